@@ -25,5 +25,11 @@ from .abi import (  # noqa: F401
     dsa3d_timing_reset,
     backward,
     forward,
+    gated_ffn,
+    gated_ffn_backward,
+    layer_norm,
+    layer_norm_backward,
     library_path,
+    rotary3d,
+    rotary3d_backward,
 )

@@ -20,6 +20,9 @@ _lock = threading.Lock()
 
 DSA3D_F32 = 0
 DSA3D_BF16 = 1
+DSA3D_SILU = 0
+DSA3D_GELU = 1
+_ACTIVATIONS = {"silu": DSA3D_SILU, "gelu": DSA3D_GELU}
 
 _STATUS = {0: "DSA3D_OK", 1: "DSA3D_ERR_INVALID_ARGUMENT", 2: "DSA3D_ERR_UNSUPPORTED",
            3: "DSA3D_ERR_WORKSPACE_TOO_SMALL", 4: "DSA3D_ERR_CUDA", 5: "DSA3D_ERR_DEVICE_CHECK"}
@@ -80,6 +83,24 @@ def _load():
         lib.dsa3d_offset_head_backward_workspace_bytes.argtypes = [I, I, I, I]
         lib.dsa3d_offset_head_backward.restype = I
         lib.dsa3d_offset_head_backward.argtypes = [P] * 11 + [Z] + [I] * 10 + [P]
+        L, FL, D = ctypes.c_longlong, ctypes.c_float, ctypes.c_double
+        lib.dsa3d_layer_norm.restype = I
+        lib.dsa3d_layer_norm.argtypes = [P] * 7 + [L, I, FL, I, P]
+        lib.dsa3d_layer_norm_backward_workspace_bytes.restype = Z
+        lib.dsa3d_layer_norm_backward_workspace_bytes.argtypes = [L, I, I]
+        lib.dsa3d_layer_norm_backward.restype = I
+        lib.dsa3d_layer_norm_backward.argtypes = [P] * 9 + [Z, L, I, I, P]
+        for f in (lib.dsa3d_rotary3d, lib.dsa3d_rotary3d_backward):
+            f.restype = I
+            f.argtypes = [P] * 4 + [L] * 6 + [I] * 5 + [I * 3, D * 3, D * 3, D, I, I, P]
+        lib.dsa3d_gated_ffn_workspace_bytes.restype = Z
+        lib.dsa3d_gated_ffn_workspace_bytes.argtypes = [L, I, I, I]
+        lib.dsa3d_gated_ffn.restype = I
+        lib.dsa3d_gated_ffn.argtypes = [P] * 7 + [Z, L, I, I, I, I, P]
+        lib.dsa3d_gated_ffn_backward_workspace_bytes.restype = Z
+        lib.dsa3d_gated_ffn_backward_workspace_bytes.argtypes = [L, I, I, I]
+        lib.dsa3d_gated_ffn_backward.restype = I
+        lib.dsa3d_gated_ffn_backward.argtypes = [P] * 10 + [Z, L, I, I, I, I, P]
         lib.dsa3d_check_device.restype = I
         lib.dsa3d_check_device.argtypes = [P]
         lib.dsa3d_timing_enable.restype = I
@@ -90,6 +111,9 @@ def _load():
         lib.dsa3d_timing_reset.argtypes = []
         _lib = lib
         return lib
+
+
+_INT3, _DBL3 = ctypes.c_int * 3, ctypes.c_double * 3
 
 
 class KernelTime(ctypes.Structure):
@@ -192,6 +216,59 @@ def dsa3d_offset_head_backward(x, dw_weight, dw_bias, pw_weight, doffsets, dx, d
                                               kt, kh, kw, dtype, stream)
 
 
+def dsa3d_layer_norm(x, add, weight, bias, y, h, stats, rows, C, eps, dtype, stream) -> int:
+    """Layer norm over the channels, with an optional fused residual sum (h = x + add)."""
+    return _load().dsa3d_layer_norm(x, add, weight, bias, y, h, stats, rows, C, eps, dtype, stream)
+
+
+def dsa3d_layer_norm_backward_workspace_bytes(rows, C, dtype) -> int:
+    return _load().dsa3d_layer_norm_backward_workspace_bytes(rows, C, dtype)
+
+
+def dsa3d_layer_norm_backward(h, weight, stats, dy, add, dx, dweight, dbias, workspace, workspace_bytes,
+                              rows, C, dtype, stream) -> int:
+    return _load().dsa3d_layer_norm_backward(h, weight, stats, dy, add, dx, dweight, dbias, workspace,
+                                             workspace_bytes, rows, C, dtype, stream)
+
+
+def dsa3d_rotary3d(q, k, q_out, k_out, ldq, ldk, ldqo, ldko, first, rows, F, Hp, Wp, heads, dh, axes,
+                   start, step, base, interleaved, dtype, stream) -> int:
+    """Rotary positions of the token grid for q and k; axes, start and step are sequences of three."""
+    return _load().dsa3d_rotary3d(q, k, q_out, k_out, ldq, ldk, ldqo, ldko, first, rows, F, Hp, Wp, heads,
+                                  dh, _INT3(*axes), _DBL3(*start), _DBL3(*step), base, interleaved, dtype,
+                                  stream)
+
+
+def dsa3d_rotary3d_backward(dq_out, dk_out, dq, dk, lddqo, lddko, lddq, lddk, first, rows, F, Hp, Wp, heads,
+                            dh, axes, start, step, base, interleaved, dtype, stream) -> int:
+    return _load().dsa3d_rotary3d_backward(dq_out, dk_out, dq, dk, lddqo, lddko, lddq, lddk, first, rows, F,
+                                           Hp, Wp, heads, dh, _INT3(*axes), _DBL3(*start), _DBL3(*step), base,
+                                           interleaved, dtype, stream)
+
+
+def dsa3d_gated_ffn_workspace_bytes(rows, C, hidden, dtype) -> int:
+    return _load().dsa3d_gated_ffn_workspace_bytes(rows, C, hidden, dtype)
+
+
+def dsa3d_gated_ffn(x, gate_weight, up_weight, down_weight, add, y, workspace, workspace_bytes, rows, C,
+                    hidden, activation, dtype, stream) -> int:
+    """y = (act(x Wg) * (x Wu)) Wd (+ add)."""
+    return _load().dsa3d_gated_ffn(x, gate_weight, up_weight, down_weight, add, y, workspace, workspace_bytes,
+                                   rows, C, hidden, activation, dtype, stream)
+
+
+def dsa3d_gated_ffn_backward_workspace_bytes(rows, C, hidden, dtype) -> int:
+    return _load().dsa3d_gated_ffn_backward_workspace_bytes(rows, C, hidden, dtype)
+
+
+def dsa3d_gated_ffn_backward(x, gate_weight, up_weight, down_weight, dy, dx, dgate_weight, dup_weight,
+                             ddown_weight, workspace, workspace_bytes, rows, C, hidden, activation, dtype,
+                             stream) -> int:
+    return _load().dsa3d_gated_ffn_backward(x, gate_weight, up_weight, down_weight, dy, dx, dgate_weight,
+                                            dup_weight, ddown_weight, workspace, workspace_bytes, rows, C,
+                                            hidden, activation, dtype, stream)
+
+
 def dsa3d_check_device(stream) -> int:
     return _load().dsa3d_check_device(stream)
 
@@ -202,9 +279,9 @@ def dsa3d_timing_enable(enable: bool) -> int:
 
 def dsa3d_timing_read() -> dict:
     """{kernel name: (launches, total ms)} accumulated since the last reset."""
-    buf = (KernelTime * 16)()
-    n = _load().dsa3d_timing_read(buf, 16)
-    return {buf[i].kernel.decode(): (int(buf[i].launches), float(buf[i].total_ms)) for i in range(min(n, 16))}
+    buf = (KernelTime * 64)()
+    n = _load().dsa3d_timing_read(buf, 64)
+    return {buf[i].kernel.decode(): (int(buf[i].launches), float(buf[i].total_ms)) for i in range(min(n, 64))}
 
 
 def dsa3d_timing_reset() -> None:
@@ -504,3 +581,215 @@ def offset_head_backward(x, dw_weight, dw_bias, pw_weight, doffsets, dims, heads
                                       C, heads, taps, kt, kh, kw, code, _stream_handle(stream)),
            "dsa3d_offset_head_backward")
     return (dx, *grads)
+
+
+# --- the transformer block around the operator -----------------------------------------------------
+def _on_stream(ref, stream, inputs):
+    """Context of a call's allocations and launches: ref's device, and the given stream where there is
+    one (the outputs and workspaces then belong to that stream).  Inputs that another stream owns are
+    recorded on it, so that freeing them right after the call is safe."""
+    torch = _torch()
+    if stream is None:
+        return torch.cuda.device(ref.device)
+    if stream.device != ref.device:
+        raise ValueError("stream and tensors must be on one device")
+    with torch.cuda.device(ref.device):
+        if stream != torch.cuda.current_stream():
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows2d(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows][C], got {tuple(t.shape)}")
+    _need(t, name, t.shape, t.dtype)
+    return t.shape
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, add=None, out=None, want_stats=True, stream=None):
+    """Layer norm of x [rows][C] over the channels, or of h = x + add [rows][C] (a residual sum, kept in
+    x's dtype); weight and bias [C] fp32 or None.  Returns (y, h, stats): h is x itself without add,
+    stats [2][rows] fp32 (means, reciprocal standard deviations; None unless want_stats) is what
+    layer_norm_backward takes."""
+    torch = _torch()
+    code = _dtype_code(x)
+    rows, C = _rows2d(x, "x")
+    if add is not None:
+        _need(add, "add", x.shape, x.dtype)
+    if weight is not None:
+        _need(weight, "weight", (C,), torch.float32)
+    if bias is not None:
+        _need(bias, "bias", (C,), torch.float32)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype)
+    _on_device(x, add, weight, bias, out)
+    with _on_stream(x, stream, (x, add, weight, bias, out)):
+        y = torch.empty_like(x) if out is None else out
+        h = None if add is None else torch.empty_like(x)
+        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device) if want_stats else None
+        _check(dsa3d_layer_norm(x.data_ptr(), _ptr(add), _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(h),
+                                _ptr(stats), rows, C, eps, code, _stream_handle(None)), "dsa3d_layer_norm")
+    return y, (x if h is None else h), stats
+
+
+def layer_norm_backward(h, weight, stats, dy, add=None, stream=None):
+    """Gradients of sum(layer_norm(h, weight, bias)[0] * dy): (dx [rows][C], dweight, dbias [C] fp32).
+    h and stats as the forward returned them; add [rows][C] is added to dx (the residual branch's
+    gradient).  Without a weight the two weight gradients are None."""
+    torch = _torch()
+    code = _dtype_code(h)
+    rows, C = _rows2d(h, "h")
+    _need(dy, "dy", h.shape, h.dtype)
+    _need(stats, "stats", (2, rows), torch.float32)
+    if add is not None:
+        _need(add, "add", h.shape, h.dtype)
+    if weight is not None:
+        _need(weight, "weight", (C,), torch.float32)
+    _on_device(h, weight, stats, dy, add)
+    with _on_stream(h, stream, (h, weight, stats, dy, add)):
+        dx = torch.empty_like(h)
+        dw = db = ws = None
+        ws_bytes = 0
+        if weight is not None:
+            dw, db = torch.empty_like(weight), torch.empty_like(weight)
+            ws_bytes = dsa3d_layer_norm_backward_workspace_bytes(rows, C, code)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=h.device)
+        _check(dsa3d_layer_norm_backward(h.data_ptr(), _ptr(weight), stats.data_ptr(), dy.data_ptr(), _ptr(add),
+                                         dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), ws_bytes, rows, C, code,
+                                         _stream_handle(None)), "dsa3d_layer_norm_backward")
+    return dx, dw, db
+
+
+def _token_stride(t, name, shape, dtype):
+    """t must be [rows][heads][dh] with contiguous heads; returns its token stride in elements."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    rows, heads, dh = shape
+    s0, s1, s2 = t.stride()
+    if (dh > 1 and s2 != 1) or (heads > 1 and s1 != dh):
+        raise ValueError(f"{name} must have contiguous [heads][dh] rows")
+    if rows > 1 and s0 < heads * dh:
+        raise ValueError(f"{name}'s tokens overlap")
+    return s0 if rows > 1 else heads * dh
+
+
+def _rotary(call, what, q, k, dims, axes, first, start, step, base, interleaved, out, stream):
+    torch = _torch()
+    code = _dtype_code(q)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [rows][heads][dh], got {tuple(q.shape)}")
+    if len(axes) != 3 or len(dims) != 3 or len(start) != 3 or len(step) != 3:
+        raise ValueError("dims, axes, start and step have three entries: frames, rows, columns")
+    rows, heads, dh = q.shape
+    ldq = _token_stride(q, "q", q.shape, q.dtype)
+    ldk = ldq if k is None else _token_stride(k, "k", q.shape, q.dtype)
+    qo, ko = (None, None) if out is None else out
+    if out is not None:
+        if (k is None) != (ko is None) or qo is None:
+            raise ValueError("out must hold one tensor for each of q and k")
+        ldqo = _token_stride(qo, "out[0]", q.shape, q.dtype)
+        ldko = ldqo if ko is None else _token_stride(ko, "out[1]", q.shape, q.dtype)
+    else:
+        ldqo = ldko = heads * dh
+    _on_device(q, k, qo, ko)
+    with _on_stream(q, stream, (q, k, qo, ko)):
+        if out is None:
+            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            ko = None if k is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _check(call(q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), ldq, ldk, ldqo, ldko, first, rows, *dims,
+                    heads, dh, axes, start, step, base, 1 if interleaved else 0, code, _stream_handle(None)),
+               what)
+    return qo, ko
+
+
+def rotary3d(q, k, dims, axes, first=0, start=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0), base=10000.0,
+             interleaved=True, out=None, stream=None):
+    """Rotary positions for q and k [rows][heads][dh] (k may be None), the tokens first .. first + rows - 1
+    of the grid dims = (F, Hp, Wp).  axes: head dims of the frame, row and column axis (even); pairs are
+    (2i, 2i+1), or (i, i + sum(axes)/2) with interleaved=False.  Positions are start + step * index.
+    Tokens may be strided (views of a packed projection); out = (q_out, k_out) may be q and k themselves.
+    Returns (q_out, k_out)."""
+    return _rotary(dsa3d_rotary3d, "dsa3d_rotary3d", q, k, dims, axes, first, start, step, base, interleaved,
+                   out, stream)
+
+
+def rotary3d_backward(dq, dk, dims, axes, first=0, start=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0), base=10000.0,
+                      interleaved=True, out=None, stream=None):
+    """Gradients of rotary3d's q and k from those of its outputs (the inverse rotation); the other
+    arguments are rotary3d's.  Returns (gradient of q, gradient of k)."""
+    return _rotary(dsa3d_rotary3d_backward, "dsa3d_rotary3d_backward", dq, dk, dims, axes, first, start, step,
+                   base, interleaved, out, stream)
+
+
+def _ffn_shapes(x, gate_weight, up_weight, down_weight, activation):
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+    rows, C = _rows2d(x, "x")
+    if gate_weight.dim() != 2 or gate_weight.shape[0] != C:
+        raise ValueError(f"gate_weight must be [C={C}][hidden], got {tuple(gate_weight.shape)}")
+    hidden = gate_weight.shape[1]
+    _need(gate_weight, "gate_weight", (C, hidden), x.dtype)
+    _need(up_weight, "up_weight", (C, hidden), x.dtype)
+    _need(down_weight, "down_weight", (hidden, C), x.dtype)
+    return rows, C, hidden
+
+
+def _ffn_workspace(workspace, need, device):
+    if isinstance(workspace, str):
+        return _torch().empty(need, dtype=_torch().uint8, device=device)
+    return workspace
+
+
+def gated_ffn(x, gate_weight, up_weight, down_weight, activation="silu", add=None, out=None, workspace="auto",
+              stream=None):
+    """Gated feed-forward block y = (act(x Wg) * (x Wu)) Wd (+ add) for x [rows][C], gate_weight and
+    up_weight [C][hidden], down_weight [hidden][C], all of x's dtype; activation "silu" or "gelu" (erf).
+    add [rows][C] is the residual branch; out may be add itself.  workspace: "auto" allocates what
+    dsa3d_gated_ffn_workspace_bytes asks for; a smaller uint8 tensor makes the call go through the
+    tokens in more chunks.  Returns y."""
+    torch = _torch()
+    code = _dtype_code(x)
+    rows, C, hidden = _ffn_shapes(x, gate_weight, up_weight, down_weight, activation)
+    if add is not None:
+        _need(add, "add", x.shape, x.dtype)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype)
+    given = None if isinstance(workspace, str) else _workspace(workspace)
+    _on_device(x, gate_weight, up_weight, down_weight, add, out, given)
+    with _on_stream(x, stream, (x, gate_weight, up_weight, down_weight, add, out, given)):
+        y = torch.empty_like(x) if out is None else out
+        ws = _ffn_workspace(workspace, dsa3d_gated_ffn_workspace_bytes(rows, C, hidden, code), x.device)
+        _check(dsa3d_gated_ffn(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), down_weight.data_ptr(),
+                               _ptr(add), y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), rows, C, hidden,
+                               _ACTIVATIONS[activation], code, _stream_handle(None)), "dsa3d_gated_ffn")
+    return y
+
+
+def gated_ffn_backward(x, gate_weight, up_weight, down_weight, dy, activation="silu", workspace="auto",
+                       stream=None):
+    """Gradients of sum(gated_ffn(x, ...) * dy): (dx, dgate_weight, dup_weight, ddown_weight), all of x's
+    dtype, from x and dy alone (x Wg and x Wu are formed again)."""
+    torch = _torch()
+    code = _dtype_code(x)
+    rows, C, hidden = _ffn_shapes(x, gate_weight, up_weight, down_weight, activation)
+    _need(dy, "dy", x.shape, x.dtype)
+    given = None if isinstance(workspace, str) else _workspace(workspace)
+    _on_device(x, gate_weight, up_weight, down_weight, dy, given)
+    with _on_stream(x, stream, (x, gate_weight, up_weight, down_weight, dy, given)):
+        grads = (torch.empty_like(x), torch.empty_like(gate_weight), torch.empty_like(up_weight),
+                 torch.empty_like(down_weight))
+        ws = _ffn_workspace(workspace, dsa3d_gated_ffn_backward_workspace_bytes(rows, C, hidden, code), x.device)
+        _check(dsa3d_gated_ffn_backward(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(),
+                                        down_weight.data_ptr(), dy.data_ptr(), *(t.data_ptr() for t in grads),
+                                        _ptr(ws), 0 if ws is None else ws.numel(), rows, C, hidden,
+                                        _ACTIVATIONS[activation], code, _stream_handle(None)),
+               "dsa3d_gated_ffn_backward")
+    return grads

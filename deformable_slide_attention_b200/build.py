@@ -23,8 +23,9 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
 def sources():
-    # the attention's translation unit, and the DWConv3D term's
-    return [os.path.join(CSRC, "dsa3d.cu"), os.path.join(CSRC, "dsa3d_conv.cu")]
+    # the attention's translation unit, the DWConv3D term's, the layer norm's and rotary positions',
+    # and the feed-forward block's
+    return [os.path.join(CSRC, f) for f in ("dsa3d.cu", "dsa3d_conv.cu", "dsa3d_block.cu", "dsa3d_ffn.cu")]
 
 
 def _stale(out):
@@ -37,7 +38,7 @@ def _stale(out):
 def build(debug: bool = False, verbose: bool = False, force: bool = False, out: str = LIB) -> str:
     if not force and not _stale(out):
         return out
-    cmd = [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [NVCC, *ARCH, "-t", "4", "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
            "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC, "-o", out + ".tmp", *sources()]
     if debug:
         cmd.insert(1, "-DDSA3D_DEBUG")

@@ -1,0 +1,50 @@
+// dsa3d_host.cuh -- host helpers of the transformer block's entry points: alignment, overlap and
+// launch-size rules shared by dsa3d_block.cu and dsa3d_ffn.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "dsa3d.h"
+#include "dsa3d_timing.cuh"
+
+namespace dsa3d {
+namespace host {
+
+inline bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) == 0; }
+inline bool aligned16(const void* p) { return aligned(p, 16); }
+inline size_t elem_size(dsa3d_dtype_t t) { return t == DSA3D_F32 ? 4 : 2; }
+inline bool known(dsa3d_dtype_t t) { return t == DSA3D_F32 || t == DSA3D_BF16; }
+
+struct Range {
+  uintptr_t lo, hi;
+};
+inline Range range_of(const void* p, size_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+  return {a, p ? a + bytes : a};
+}
+inline bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+inline int sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 1;
+  return sms > 0 ? sms : 1;
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// One launch inside the optional per-kernel timer.
+template <typename F>
+dsa3d_status_t launch(int kernel_id, cudaStream_t st, F&& f) {
+  TimedLaunch tl(kernel_id, st);
+  f();
+  const bool launched = cudaGetLastError() == cudaSuccess;
+  return (tl.finish() && launched) ? DSA3D_OK : DSA3D_ERR_CUDA;
+}
+
+}  // namespace host
+}  // namespace dsa3d

@@ -37,6 +37,14 @@ enum KernelId {
   kKernBwdDqTc,
   kKernDwconvSw,
   kKernDwconvSw2,
+  kKernLayerNorm,
+  kKernLayerNormBwd,
+  kKernNormReduce,
+  kKernRotary,
+  kKernFfnAny,
+  kKernFfnReduce,
+  kKernFfnTc,
+  kKernFfnSkinny,
   kKernCount
 };
 inline const char* kernel_name(int id) {
@@ -49,7 +57,9 @@ inline const char* kernel_name(int id) {
       "dsa3d_dwconv3d_dw_kernel", "dsa3d_pointwise_offsets_kernel", "dsa3d_pointwise_dz_kernel",
       "dsa3d_pointwise_dw_kernel", "dsa3d_sort_order_kernels", "dsa3d_fwd_tc_kernel",
       "dsa3d_bwd_kv_tc_kernel", "dsa3d_bwd_dq_tc_kernel", "dsa3d_dwconv3d_sw_kernel",
-      "dsa3d_dwconv3d_sw2_kernel"};
+      "dsa3d_dwconv3d_sw2_kernel", "dsa3d_layer_norm_kernel", "dsa3d_layer_norm_bwd_kernel",
+      "dsa3d_norm_reduce_kernel", "dsa3d_rotary_kernel", "dsa3d_ffn_any_kernel",
+      "dsa3d_ffn_reduce_kernel", "dsa3d_ffn_tc_kernel", "dsa3d_ffn_skinny_kernel"};
   return names[id];
 }
 

@@ -262,6 +262,110 @@ dsa3d_status_t dsa3d_offset_head(const void *x, const float *dw_weight, const fl
                                  dsa3d_dtype_t dtype, cudaStream_t stream);
 
 /*
+ * The operators of the transformer block around 3D-DSA (MegaSlide-DiT builds its blocks from 3D-DSA,
+ * an MLP, layer norm and residual sums): layer norm, rotary positions of the token grid for q and k,
+ * and a gated feed-forward block, each with its backward pass.  Rows are tokens; rows = 0 is a valid
+ * empty call (weight gradients are then zero, everything else is left alone).
+ */
+
+/*
+ * Layer norm over the channels of each token.
+ *   x, add   [rows][C] I/O type (add may be NULL);  weight, bias [C] fp32 (both may be NULL; a bias
+ *            needs a weight);  eps >= 0, finite;
+ *   h        [rows][C] I/O type (written): x + add rounded to the I/O type; NULL exactly when add is
+ *            (then h is x itself).  May be x or add (in place);
+ *   y        [rows][C] I/O type (written): (h - mean) * rstd * weight + bias;
+ *   stats    [2][rows] fp32 (written; may be NULL): the means, then rstd = (variance + eps)^(-1/2).
+ * Statistics and sums are fp32; the variance is the centred one.  1 <= C <= 16384; rows that are no
+ * multiple of 16 bytes: C <= 8192.  rows < 2^31.
+ */
+dsa3d_status_t dsa3d_layer_norm(const void *x, const void *add, const float *weight, const float *bias,
+                                void *y, void *h, float *stats, long long rows, int C, float eps,
+                                dsa3d_dtype_t dtype, cudaStream_t stream);
+
+/* Bytes of workspace dsa3d_layer_norm_backward needs when it has a weight (it needs none without). */
+size_t dsa3d_layer_norm_backward_workspace_bytes(long long rows, int C, dsa3d_dtype_t dtype);
+
+/*
+ * Backward of dsa3d_layer_norm for the upstream gradient dy [rows][C]: h and stats as the forward
+ * left them (h = x there without an add);
+ *   dx       [rows][C] I/O type (written): the gradient with respect to h, plus add [rows][C] if given
+ *            (the residual branch's gradient); may be add itself;
+ *   dweight, dbias [C] fp32 (written): given exactly when weight is.  Summed over all rows in fp32,
+ *            in an order that depends on the sizes and the GPU's SM count only.
+ */
+dsa3d_status_t dsa3d_layer_norm_backward(const void *h, const float *weight, const float *stats,
+                                         const void *dy, const void *add, void *dx, float *dweight,
+                                         float *dbias, void *workspace, size_t workspace_bytes,
+                                         long long rows, int C, dsa3d_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Rotary positions with three axes for q and k [rows][heads][dh] (I/O type), the tokens first ..
+ * first + rows - 1 of an F x Hp x Wp grid (n = (t*Hp + y)*Wp + x): a whole grid, a shard of it, a
+ * frame or a single token.
+ *   axes[3]: dims of the frame, row and column axis (even, >= 0; their sum R in 2..dh); the R/2 pairs
+ *            are shared out in this order.  Pair i is dims (2i, 2i+1) with interleaved != 0, else
+ *            (i, i + R/2); dims from R on are copied unchanged.
+ *   Pair j of axis a turns by theta = (start[a] + step[a] * index_a) * base^(-2j / axes[a]):
+ *   (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos).  start and step shift and scale the grid (a clip
+ *   inside a longer video, a lower resolution); angles are fp64, their sines and cosines fp32.
+ *   ldq, ldk, ldqo, ldko: token strides in elements, >= heads*dh (q and k may be read out of a packed
+ *   projection, and written into one).  Pointers are aligned to their elements here; 16-byte aligned
+ *   pointers, strides and heads take the vector kernel.  q_out may be q, and k_out k, with the same
+ *   stride (in place); k and k_out may both be NULL.  axes, start and step are host arrays.
+ * dh even, 2..256; F*Hp*Wp < 2^31; |start| + |step| * extent <= 2^40.
+ */
+dsa3d_status_t dsa3d_rotary3d(const void *q, const void *k, void *q_out, void *k_out, long long ldq,
+                              long long ldk, long long ldqo, long long ldko, long long first,
+                              long long rows, int F, int Hp, int Wp, int heads, int dh, const int *axes,
+                              const double *start, const double *step, double base, int interleaved,
+                              dsa3d_dtype_t dtype, cudaStream_t stream);
+
+/* Backward: the gradients of q and k from those of the rotated ones (the inverse rotation). */
+dsa3d_status_t dsa3d_rotary3d_backward(const void *dq_out, const void *dk_out, void *dq, void *dk,
+                                       long long lddqo, long long lddko, long long lddq, long long lddk,
+                                       long long first, long long rows, int F, int Hp, int Wp, int heads,
+                                       int dh, const int *axes, const double *start, const double *step,
+                                       double base, int interleaved, dsa3d_dtype_t dtype,
+                                       cudaStream_t stream);
+
+/*
+ * Gated feed-forward block: y = (act(x Wg) * (x Wu)) Wd (+ add).
+ *   x, y, add [rows][C] (add may be NULL; y may be add);  gate_weight Wg, up_weight Wu [C][hidden],
+ *   down_weight Wd [hidden][C], all in the I/O type;  act: silu(g) = g / (1 + e^-g), or gelu(g) =
+ *   g Phi(g) with the normal distribution Phi (erf, not the tanh form).
+ * Sums are fp32; act(x Wg) * (x Wu) is rounded to the I/O type once, as the operand of the second
+ * product.  rows < 2^31, C and hidden <= 2^20.
+ * The workspace holds a chunk of tokens' hidden values; the size dsa3d_gated_ffn_workspace_bytes
+ * returns covers min(rows, 65536) tokens, and any workspace of at least the size for min(rows, 256)
+ * works (tokens are then processed in more chunks).
+ */
+typedef enum { DSA3D_SILU = 0, DSA3D_GELU = 1 } dsa3d_activation_t;
+
+size_t dsa3d_gated_ffn_workspace_bytes(long long rows, int C, int hidden, dsa3d_dtype_t dtype);
+dsa3d_status_t dsa3d_gated_ffn(const void *x, const void *gate_weight, const void *up_weight,
+                               const void *down_weight, const void *add, void *y, void *workspace,
+                               size_t workspace_bytes, long long rows, int C, int hidden,
+                               dsa3d_activation_t activation, dsa3d_dtype_t dtype, cudaStream_t stream);
+
+/*
+ * Backward of dsa3d_gated_ffn for the upstream gradient dy [rows][C], from x alone: the forward keeps
+ * nothing of [rows][hidden] (two such tensors would be larger than the GPU's memory at long-video
+ * sizes), so x Wg and x Wu are formed again.
+ *   dx [rows][C], dgate_weight, dup_weight [C][hidden], ddown_weight [hidden][C], I/O type (written;
+ *   sums over tokens are fp32, rounded once).  add's gradient is dy itself.
+ * The workspace rule is the forward's, with dsa3d_gated_ffn_backward_workspace_bytes; the result of
+ * the weight gradients may differ in the last bits between chunk sizes (another order of summation).
+ */
+size_t dsa3d_gated_ffn_backward_workspace_bytes(long long rows, int C, int hidden, dsa3d_dtype_t dtype);
+dsa3d_status_t dsa3d_gated_ffn_backward(const void *x, const void *gate_weight, const void *up_weight,
+                                        const void *down_weight, const void *dy, void *dx,
+                                        void *dgate_weight, void *dup_weight, void *ddown_weight,
+                                        void *workspace, size_t workspace_bytes, long long rows, int C,
+                                        int hidden, dsa3d_activation_t activation, dsa3d_dtype_t dtype,
+                                        cudaStream_t stream);
+
+/*
  * Synchronises `stream` and reports DSA3D_ERR_DEVICE_CHECK if any kernel of this library on the
  * current device recorded a failed internal check since the last call (the record is then
  * cleared), DSA3D_ERR_CUDA if the stream reports an error, else DSA3D_OK.
