@@ -77,7 +77,7 @@ TENSOR_CORE_FILES = ["dsa3d.cu", "dsa3d_common.cuh", "dsa3d_tc.cuh", "dsa3d_sort
                      "dsa3d_fwd_mma.cuh", "dsa3d_bwd_mma.cuh", "dsa3d_bwd_dq_tc.cuh", "dsa3d_bwd_kv_tc.cuh"]
 PER_TAP_FILES = ["dsa3d.cu", "dsa3d_common.cuh", "dsa3d_taps.cuh", "dsa3d_bwd.cuh", "dsa3d_fwd.cuh"]
 NCU_TRAFFIC = [
-    {"files": TENSOR_CORE_FILES, "sources": "415297fb73f643fa",
+    {"files": TENSOR_CORE_FILES, "sources": "f50dae36517b6936",
      "capture": "profiles/tensor_core_kernels_720p-train-bf16.md",
      "bytes_per_item": {
          "dsa3d_fwd_tc_kernel": 1020.1,
@@ -85,7 +85,7 @@ NCU_TRAFFIC = [
          "dsa3d_bwd_dq_tc_kernel": 1701.6,
          "dsa3d_bwd_kv_tc_kernel": 2136.1,
      }},
-    {"files": PER_TAP_FILES, "sources": "df10cf32e12d6270",
+    {"files": PER_TAP_FILES, "sources": "b5943fdf2e2a52cd",
      "capture": "profiles/per_tap_kernels_720p-train-taps-bf16.md",
      "bytes_per_item": {
          "dsa3d_fwd_taps_kernel": 18471.7,

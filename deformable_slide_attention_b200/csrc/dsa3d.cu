@@ -772,6 +772,9 @@ dsa3d_status_t noalloc_scratch(void** out) {
 }  // namespace
 }  // namespace dsa3d
 
+namespace dsa3d {
+bool ffn_device_check(int* flag);  // dsa3d_ffn.cu
+}
 using namespace dsa3d;
 
 extern "C" {
@@ -1039,14 +1042,14 @@ int dsa3d_tc_clk_read(unsigned* host, int n) {
 
 dsa3d_status_t dsa3d_check_device(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return DSA3D_ERR_CUDA;
-  int flag = 0;
+  int flag = 0, ffn_flag = 0;
   if (cudaMemcpyFromSymbol(&flag, g_dsa3d_check, sizeof(int)) != cudaSuccess) return DSA3D_ERR_CUDA;
+  if (!ffn_device_check(&ffn_flag)) return DSA3D_ERR_CUDA;
   if (flag) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_dsa3d_check, &zero, sizeof(int)) != cudaSuccess) return DSA3D_ERR_CUDA;
-    return DSA3D_ERR_DEVICE_CHECK;
   }
-  return DSA3D_OK;
+  return flag || ffn_flag ? DSA3D_ERR_DEVICE_CHECK : DSA3D_OK;
 }
 
 }  // extern "C"

@@ -206,9 +206,9 @@ __device__ __forceinline__ void unpack3(int r, int& a, int& b, int& c) {
 }
 
 // Device-side check record (set by kernels built with DSA3D_DEBUG, read by dsa3d_check_device).
-// Of the library's two translation units only dsa3d.cu includes this header (the convolution's
-// dsa3d_conv.cu does not), so this is its only definition.
-__device__ int g_dsa3d_check;
+// Each translation unit that includes this header (dsa3d.cu, dsa3d_ffn.cu) has a record of its own;
+// dsa3d_check_device reads both.
+static __device__ int g_dsa3d_check;
 
 #ifdef DSA3D_DEBUG
 #define DSA3D_DEVICE_CHECK(cond) \
