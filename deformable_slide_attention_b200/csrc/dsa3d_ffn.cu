@@ -1,7 +1,7 @@
 // dsa3d_ffn.cu -- C ABI of the gated feed-forward block (include/dsa3d.h): argument validation, the
 // plan of a call (tokens per chunk, splits, workspace) and the launches.  The kernels are in
-// dsa3d_ffn_tc.cuh (tensor cores: bf16, C and hidden multiples of 8) and dsa3d_ffn_any.cuh (CUDA cores:
-// everything else).  This file allocates no device memory.
+// dsa3d_ffn_tc.cuh (bf16, tensor cores) and dsa3d_ffn_f32.cuh (fp32, CUDA cores; and the joining of
+// split sums).  This file allocates no device memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -12,7 +12,7 @@
 #include <mutex>
 
 #include "dsa3d.h"
-#include "dsa3d_ffn_any.cuh"
+#include "dsa3d_ffn_f32.cuh"
 #include "dsa3d_ffn_tc.cuh"
 #include "dsa3d_host.cuh"
 
@@ -21,9 +21,11 @@ namespace {
 
 using namespace host;
 
+using bf16 = __nv_bfloat16;
+
 constexpr int64_t kFfnChunk = 65536;    // tokens per chunk of a full-size workspace
 constexpr int64_t kFfnMinChunk = 256;   // and of the smallest one
-constexpr int kFfnMaxSplits = 32;
+constexpr int kFfnMaxParts = 32;
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
@@ -31,7 +33,15 @@ struct Ffn {
   int64_t rows;
   int C, hidden, act;
   dsa3d_dtype_t dtype;
+  bool f32() const { return dtype == DSA3D_F32; }
   size_t es() const { return elem_size(dtype); }
+  // Row strides of the bf16 tensors that TMA reads: multiples of 16 bytes.  Tensors whose rows are not
+  // are copied into the workspace first.
+  int64_t ldc() const { return f32() ? C : (C + 7) / 8 * 8; }
+  int64_t ldh() const { return f32() ? hidden : (hidden + 7) / 8 * 8; }
+  // Row stride of the hidden values in the workspace: whole 128-byte lines (the products' boxes are 128
+  // bytes wide; at hidden = 5464 rows of 10,928 bytes cost dx's product a quarter more L2 sectors).
+  int64_t ldw() const { return f32() ? hidden : ((int64_t)hidden + 63) / 64 * 64; }
 };
 
 dsa3d_status_t check_ffn_shape(long long rows, int C, int hidden, dsa3d_dtype_t dtype) {
@@ -40,58 +50,173 @@ dsa3d_status_t check_ffn_shape(long long rows, int C, int hidden, dsa3d_dtype_t 
   return DSA3D_OK;
 }
 
-// Parts of the summed axis for a weight gradient [C][hidden] summed over `tokens`: enough blocks for
-// two per SM, each with 256 tokens or more.
-int any_splits(const Ffn& f, int64_t tokens) {
-  const int64_t tiles = ceil_div(f.C, kAnyTile) * ceil_div(f.hidden, kAnyTile);
-  const int64_t want = ceil_div(296, tiles);
-  return (int)std::max<int64_t>(1, std::min<int64_t>({want, tokens / 256, (int64_t)kFfnMaxSplits}));
+// --- plan: parts of a summed axis, and the workspace -------------------------------------------------
+int64_t tiles_for(int64_t m, int64_t n, int tile_m, int tile_n) { return ceil_div(m, tile_m) * ceil_div(n, tile_n); }
+
+// fp32.  Parts: as many as keep two blocks per SM busy when the tiles alone do not, each of 128 of the
+// summed axis or more, none empty.
+int f32_parts(int64_t tiles, int64_t len) {
+  const int64_t slots = 2 * sm_count(), steps = ceil_div(len, kF32K);
+  if (tiles >= slots) return 1;
+  const int64_t p = std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 8, (int64_t)kFfnMaxParts}));
+  return (int)ceil_div(steps, ceil_div(steps, p));
+}
+int f32_out_parts(const Ffn& f, int64_t rows) { return f32_parts(tiles_for(rows, f.C, kF32Tile, kF32Tile), f.hidden); }
+int f32_dw_parts(const Ffn& f, int64_t rows) {
+  return f32_parts(3 * tiles_for(f.C, f.hidden, kF32Tile, kF32Tile), rows);
 }
 
-// The tensor-core path: bf16 rows of whole 16-byte units, which TMA's strides need.
-bool use_tc(const Ffn& f) { return f.dtype == DSA3D_BF16 && f.C % 8 == 0 && f.hidden % 8 == 0; }
-
-// CTAs per tile: pairs, unless the rows fill no more than one CTA's 128.
+// CTAs per tensor-core tile: pairs, unless the rows fill no more than one CTA's 128.
 int tc_pair(int64_t rows) { return rows > 128 ? 2 : 1; }
 
-int64_t tc_tiles(int64_t m, int64_t n, int cg, int tile_n) { return ceil_div(m, 128 * cg) * ceil_div(n, tile_n); }
-
-// Parts of the summed axis (k-blocks of 64): as many as keep every CTA (pair) busy when the tiles alone
-// do not, each of 4 k-blocks or more (a part's sums cross memory in fp32 once more).
-int tc_parts(int64_t tiles, int64_t kblocks, int cg) {
+// Numbers the tiles of M x N outputs and chooses the tail (FtTiles): the tiles of the last, partly empty
+// round of CTAs, cut into the number of parts that shortens that round most.  A k-block of a 256-wide
+// tile takes about 0.3 us; the joining launch about 6.
+FtTiles tc_tiles(int problems, const int64_t (&M)[3], const int64_t (&N)[3], int cg, int64_t kblocks, int products,
+                 bool all_tail) {
+  FtTiles t{};
+  int64_t tiles = 0;
+  for (int p = 0; p < problems; p++) {
+    t.M[p] = M[p];
+    t.N[p] = N[p];
+    t.tiles_m[p] = (int)ceil_div(M[p], 128 * cg);
+    t.tiles_of[p] = t.tiles_m[p] * (int)ceil_div(N[p], 256);
+    tiles += t.tiles_of[p];
+  }
+  t.problems = problems;
+  t.group = 16 / cg;
+  t.kblocks = (int)kblocks;
   const int64_t slots = std::max(1, sm_count() / cg);
-  if (tiles >= slots) return 1;
-  const int64_t p = std::max<int64_t>(1, std::min<int64_t>({slots / tiles, kblocks / 4, (int64_t)kFfnMaxSplits}));
-  return (int)ceil_div(kblocks, ceil_div(kblocks, p));  // no empty part
+  const int64_t tail = all_tail ? tiles : tiles % slots;
+  const double rounds = (double)ceil_div(tail, slots);
+  double best = rounds;
+  int64_t parts = 1;
+  for (int64_t p = 2; p <= kFfnMaxParts && p <= kblocks / 4 && tail < slots; p++) {
+    if (ceil_div(kblocks, ceil_div(kblocks, p)) != p) continue;  // an empty part
+    const double r = (double)ceil_div(tail * p, slots) / p + 0.01 * p;  // the parts' sums cross memory
+    if (r < best) {
+      best = r;
+      parts = p;
+    }
+  }
+  if (!all_tail && (rounds - best) * kblocks * products * 0.3 < 6.0) parts = 1;
+  t.full = (all_tail || parts > 1) ? tiles - tail : tiles;
+  t.parts = (int)parts;
+  t.per_part = (int)ceil_div(kblocks, parts);
+  t.units = t.full + (tiles - t.full) * parts;
+  return t;
 }
-int tc_out_parts(const Ffn& f, int64_t rows) {  // y, and dx, [rows][C] summed over hidden
-  const int cg = tc_pair(rows);
-  return tc_parts(tc_tiles(rows, f.C, cg, 256), ceil_div(f.hidden, kFtK), cg);
-}
-int64_t tc_dw_tiles(const Ffn& f) {
-  return 2 * tc_tiles(f.C, f.hidden, 2, 256) + tc_tiles(f.hidden, f.C, 2, 256);
-}
-int tc_dw_parts(const Ffn& f, int64_t rows) { return tc_parts(tc_dw_tiles(f), ceil_div(rows, kFtK), 2); }
+int64_t sums_elems(const FtTiles& t, int cg) { return (t.units - t.full) * 128 * cg * 256; }
 
-size_t out_partial_bytes(const Ffn& f, int64_t rows) {
-  const int parts = tc_out_parts(f, rows);
-  return parts > 1 ? align256((size_t)parts * rows * f.C * 4) : 0;
+// y (one product) and dx (two): [rows][C] summed over hidden.
+FtTiles tc_out_tiles(const Ffn& f, int64_t rows, int products) {
+  const int64_t M[3] = {rows}, N[3] = {f.C};
+  return tc_tiles(1, M, N, tc_pair(rows), ceil_div(f.hidden, kFtK), products, f.ldc() != f.C);
 }
-size_t fwd_bytes(const Ffn& f, int64_t chunk) {
-  size_t b = align256((size_t)chunk * f.hidden * f.es());
-  if (use_tc(f)) b += out_partial_bytes(f, chunk);
-  return b;
+// The three weight gradients, summed over tokens.
+FtTiles tc_dw_tiles(const Ffn& f, int64_t rows, bool all_tail) {
+  const int64_t M[3] = {f.C, f.C, f.hidden}, N[3] = {f.hidden, f.hidden, f.C};
+  return tc_tiles(3, M, N, 2, ceil_div(rows, kFtK), 1, all_tail);
 }
-size_t bwd_bytes(const Ffn& f, int64_t chunk) {
-  const size_t hid = 3 * align256((size_t)chunk * f.hidden * f.es()), w = (size_t)3 * f.C * f.hidden * 4;
-  if (!use_tc(f)) return hid + align256((size_t)any_splits(f, chunk) * w);
-  // weight-gradient sums in fp32 when tokens come in parts or chunks; dx's parts use the space after them,
-  // since the sums live on from chunk to chunk
-  const int parts = tc_dw_parts(f, chunk);
-  return hid + ((parts > 1 || chunk < f.rows) ? align256(parts * w) : 0) + out_partial_bytes(f, chunk);
+// The hidden values: tiles of tile_n columns, all whole.
+FtTiles tc_hidden_tiles(const Ffn& f, int64_t rows, int tile_n) {
+  FtTiles t{};
+  t.M[0] = rows;
+  t.N[0] = f.hidden;
+  t.tiles_m[0] = (int)ceil_div(rows, 128 * tc_pair(rows));
+  t.tiles_of[0] = t.tiles_m[0] * (int)ceil_div(f.hidden, tile_n);
+  t.problems = 1;
+  t.group = 16 / tc_pair(rows);
+  t.kblocks = (int)ceil_div(f.C, kFtK);
+  t.parts = 1;
+  t.full = t.units = t.tiles_of[0];
+  return t;
 }
 
-// The largest chunk whose workspace fits: all rows, or a multiple of kFfnMinChunk; 0 when none does.
+// Hands out pieces of the workspace in order; with a null base it only counts.
+struct Carver {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(bool wanted, size_t elems) {
+    if (!wanted) return nullptr;
+    T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += align256(elems * sizeof(T));
+    return p;
+  }
+};
+
+struct FwdWs {
+  char* h;                     // [chunk][ldw]
+  bf16 *x, *wg, *wu, *wd;      // copies with 16-byte rows, where the tensors have none
+  float* sums;                 // y's split sums: fp32 [parts][chunk][C], bf16 the tail's tiles
+  size_t sums_elems, bytes;
+};
+FwdWs fwd_ws(const Ffn& f, int64_t chunk, void* base) {
+  Carver c{static_cast<char*>(base)};
+  FwdWs w;
+  const bool padc = f.ldc() != f.C, padh = f.ldh() != f.hidden;
+  w.h = c.take<char>(true, (size_t)chunk * f.ldw() * f.es());
+  w.x = c.take<bf16>(padc, (size_t)chunk * f.ldc());
+  w.wg = c.take<bf16>(padh, (size_t)f.C * f.ldh());
+  w.wu = c.take<bf16>(padh, (size_t)f.C * f.ldh());
+  w.wd = c.take<bf16>(padc, (size_t)f.hidden * f.ldc());
+  if (f.f32()) {
+    const int parts = f32_out_parts(f, chunk);
+    w.sums_elems = parts > 1 ? (size_t)parts * chunk * f.C : 0;
+  } else {
+    w.sums_elems = (size_t)sums_elems(tc_out_tiles(f, chunk, 1), tc_pair(chunk));
+  }
+  w.sums = c.take<float>(w.sums_elems > 0, w.sums_elems);
+  w.bytes = c.used;
+  return w;
+}
+
+struct BwdWs {
+  char *dg, *du, *h;                // [chunk][ldw]
+  bf16 *x, *dy, *wg, *wu, *wd;      // copies with 16-byte rows
+  float* dw[3];                     // the weight gradients' split sums (bf16: dw[0], the tail's tiles of all three)
+  float* sums;                      // dx's
+  size_t sums_elems, bytes;
+  bool dw_sums;                     // fp32: the weight gradients go through dw
+};
+// bf16 weight gradients whose sums all go through the workspace: several chunks, or rows TMA cannot store.
+bool dw_all_tail(const Ffn& f, int64_t chunk) {
+  return chunk < f.rows || f.ldc() != f.C || f.ldh() != f.hidden;
+}
+BwdWs bwd_ws(const Ffn& f, int64_t chunk, void* base) {
+  Carver c{static_cast<char*>(base)};
+  BwdWs w;
+  const bool padc = f.ldc() != f.C, padh = f.ldh() != f.hidden;
+  const size_t hid = (size_t)chunk * f.ldw() * f.es();
+  w.dg = c.take<char>(true, hid);
+  w.du = c.take<char>(true, hid);
+  w.h = c.take<char>(true, hid);
+  w.x = c.take<bf16>(padc, (size_t)chunk * f.ldc());
+  w.dy = c.take<bf16>(padc, (size_t)chunk * f.ldc());
+  w.wg = c.take<bf16>(padh, (size_t)f.C * f.ldh());
+  w.wu = c.take<bf16>(padh, (size_t)f.C * f.ldh());
+  w.wd = c.take<bf16>(padc, (size_t)f.hidden * f.ldc());
+  w.dw_sums = false;
+  w.dw[0] = w.dw[1] = w.dw[2] = nullptr;
+  if (f.f32()) {
+    const int dparts = f32_dw_parts(f, chunk), parts = f32_out_parts(f, chunk);
+    w.dw_sums = dparts > 1 || chunk < f.rows;
+    for (int i = 0; i < 3; i++) w.dw[i] = c.take<float>(w.dw_sums, (size_t)dparts * f.C * f.hidden);
+    w.sums_elems = parts > 1 ? (size_t)parts * chunk * f.C : 0;
+  } else {
+    const size_t n = (size_t)sums_elems(tc_dw_tiles(f, chunk, dw_all_tail(f, chunk)), 2);
+    w.dw[0] = c.take<float>(n > 0, n);
+    w.sums_elems = (size_t)sums_elems(tc_out_tiles(f, chunk, 2), tc_pair(chunk));
+  }
+  w.sums = c.take<float>(w.sums_elems > 0, w.sums_elems);
+  w.bytes = c.used;
+  return w;
+}
+size_t fwd_bytes(const Ffn& f, int64_t chunk) { return fwd_ws(f, chunk, nullptr).bytes; }
+size_t bwd_bytes(const Ffn& f, int64_t chunk) { return bwd_ws(f, chunk, nullptr).bytes; }
+
+// A chunk whose workspace fits: all rows, or a multiple of kFfnMinChunk; 0 when none does.
 template <typename Bytes>
 int64_t fit_chunk(const Ffn& f, size_t have, Bytes bytes) {
   if (f.rows <= kFfnChunk && bytes(f, f.rows) <= have) return f.rows;
@@ -108,113 +233,141 @@ int64_t fit_chunk(const Ffn& f, size_t have, Bytes bytes) {
 
 template <typename T>
 const T* at_row(const void* p, int64_t row, int64_t width) {
-  return static_cast<const T*>(p) + row * width;
+  return p ? static_cast<const T*>(p) + row * width : nullptr;
 }
-
-template <typename T, int MODE>
-dsa3d_status_t any_launch(const AnyArgs& a, int splits, cudaStream_t st) {
-  const int64_t tiles = ceil_div(a.M, kAnyTile) * ceil_div(a.N, kAnyTile);
-  if (tiles > INT_MAX) return DSA3D_ERR_UNSUPPORTED;
-  return launch(kKernFfnAny, st, [&] {
-    dsa3d_ffn_any_kernel<T, MODE><<<dim3((unsigned)tiles, (unsigned)splits), kAnyThreads, 0, st>>>(a);
-  });
-}
-
 template <typename T>
-dsa3d_status_t reduce_launch(const float* partial, int splits, int64_t stride, const void* add, void* out,
-                             int64_t n, cudaStream_t st) {
-  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(n, 256), (int64_t)sm_count() * 8);
-  return launch(kKernFfnReduce, st, [&] {
-    dsa3d_ffn_reduce_kernel<T><<<grid, 256, 0, st>>>(partial, splits, stride, static_cast<const T*>(add),
-                                                     static_cast<T*>(out), n);
-  });
+T* at_row(void* p, int64_t row, int64_t width) {
+  return p ? static_cast<T*>(p) + row * width : nullptr;
 }
 
 struct FfnFwd {
   const void *x, *wg, *wu, *wd, *add;
   void *y, *ws;
 };
-
-template <typename T>
-dsa3d_status_t any_forward(const Ffn& f, const FfnFwd& p, int64_t chunk, cudaStream_t st) {
-  for (int64_t r0 = 0; r0 < f.rows; r0 += chunk) {
-    const int64_t n = std::min(chunk, f.rows - r0);
-    const T* x = at_row<T>(p.x, r0, f.C);
-    AnyArgs a{};
-    a.A[0] = a.A[1] = {x, f.C, 1};
-    a.B[0] = {p.wg, 1, f.hidden};
-    a.B[1] = {p.wu, 1, f.hidden};
-    a.out[0] = p.ws;
-    a.M = n; a.N = f.hidden; a.K = f.C;
-    a.act = f.act;
-    dsa3d_status_t rc = any_launch<T, kAnyHidden>(a, 1, st);
-    if (rc != DSA3D_OK) return rc;
-    AnyArgs b{};
-    b.A[0] = {p.ws, f.hidden, 1};
-    b.B[0] = {p.wd, 1, f.C};
-    b.add = p.add ? at_row<T>(p.add, r0, f.C) : nullptr;
-    b.out[0] = const_cast<T*>(at_row<T>(p.y, r0, f.C));
-    b.M = n; b.N = f.C; b.K = f.hidden;
-    b.products = 1;
-    if ((rc = any_launch<T, kAnyOut>(b, 1, st)) != DSA3D_OK) return rc;
-  }
-  return DSA3D_OK;
-}
-
 struct FfnBwd {
   const void *x, *wg, *wu, *wd, *dy;
   void *dx, *dwg, *dwu, *dwd, *ws;
 };
 
-template <typename T>
-dsa3d_status_t any_backward(const Ffn& f, const FfnBwd& p, int64_t chunk, cudaStream_t st) {
-  const int splits = any_splits(f, chunk);
-  const size_t hb = align256((size_t)chunk * f.hidden * sizeof(T));
-  char* ws = static_cast<char*>(p.ws);
-  T *dg = reinterpret_cast<T*>(ws), *du = reinterpret_cast<T*>(ws + hb), *h = reinterpret_cast<T*>(ws + 2 * hb);
-  float* partial = reinterpret_cast<float*>(ws + 3 * hb);
-  const int64_t wn = (int64_t)f.C * f.hidden;
+// --- fp32 -------------------------------------------------------------------------------------------
+template <int MODE>
+dsa3d_status_t f32_launch(const F32Batch& b, int problems, cudaStream_t st) {
+  int64_t tiles = 0;
+  for (int i = 0; i < problems; i++) tiles = std::max(tiles, tiles_for(b.p[i].M, b.p[i].N, kF32Tile, kF32Tile));
+  if (tiles > INT_MAX) return DSA3D_ERR_UNSUPPORTED;
+  return launch(kKernFfnF32, st, [&] {
+    dsa3d_ffn_f32_kernel<MODE><<<dim3((unsigned)tiles, b.p[0].parts, problems), kF32Threads, 0, st>>>(b);
+  });
+}
+
+dsa3d_status_t f32_join(const F32Join& r, int outputs, cudaStream_t st) {
+  int64_t most = 0;
+  for (int i = 0; i < outputs; i++) most = std::max(most, r.n[i]);
+  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(most, 256), (int64_t)sm_count() * 8);
+  return launch(kKernFfnReduce, st, [&] { dsa3d_ffn_join_kernel<<<dim3(grid, outputs), 256, 0, st>>>(r); });
+}
+
+// y or dx from up to two products over hidden, in parts where the plan has them.
+dsa3d_status_t f32_out(const Ffn& f, F32Batch& b, int64_t n, float* sum, int parts, const float* add, float* out,
+                       cudaStream_t st) {
+  F32Args& a = b.p[0];
+  a.M = n; a.N = f.C; a.K = f.hidden;
+  a.parts = parts;
+  a.out[0] = parts > 1 ? sum : out;
+  a.add = parts > 1 ? nullptr : add;
+  const dsa3d_status_t rc = f32_launch<kF32Sum>(b, 1, st);
+  if (rc != DSA3D_OK || parts == 1) return rc;
+  F32Join r{};
+  r.partial[0] = sum; r.add = add; r.out[0] = out;
+  r.n[0] = n * f.C;
+  r.parts = parts;
+  return f32_join(r, 1, st);
+}
+
+dsa3d_status_t f32_forward(const Ffn& f, const FfnFwd& p, int64_t chunk, cudaStream_t st) {
+  const int64_t C = f.C, H = f.hidden;
+  const FwdWs w = fwd_ws(f, chunk, p.ws);
+  const int parts = f32_out_parts(f, chunk);  // of every chunk, the last and shorter one too
+  float* h = reinterpret_cast<float*>(w.h);
+  const float *wg = static_cast<const float*>(p.wg), *wu = static_cast<const float*>(p.wu),
+              *wd = static_cast<const float*>(p.wd);
+  for (int64_t r0 = 0; r0 < f.rows; r0 += chunk) {
+    const int64_t n = std::min(chunk, f.rows - r0);
+    const float* x = at_row<float>(p.x, r0, C);
+    F32Batch b{};
+    F32Args& a = b.p[0];
+    a.A[0] = a.A[1] = {x, C, 1};
+    a.B[0] = {wg, 1, H};
+    a.B[1] = {wu, 1, H};
+    a.out[0] = h;
+    a.M = n; a.N = H; a.K = C;
+    a.parts = 1; a.act = f.act;
+    dsa3d_status_t rc = f32_launch<kF32Hidden>(b, 1, st);
+    if (rc != DSA3D_OK) return rc;
+    F32Batch o{};
+    o.p[0].A[0] = {h, H, 1};
+    o.p[0].B[0] = {wd, 1, C};
+    o.p[0].products = 1;
+    rc = f32_out(f, o, n, w.sums, parts, at_row<float>(p.add, r0, C), at_row<float>(p.y, r0, C), st);
+    if (rc != DSA3D_OK) return rc;
+  }
+  return DSA3D_OK;
+}
+
+dsa3d_status_t f32_backward(const Ffn& f, const FfnBwd& p, int64_t chunk, cudaStream_t st) {
+  const int64_t C = f.C, H = f.hidden;
+  const BwdWs w = bwd_ws(f, chunk, p.ws);
+  float *dg = reinterpret_cast<float*>(w.dg), *du = reinterpret_cast<float*>(w.du), *h = reinterpret_cast<float*>(w.h);
+  const float *wg = static_cast<const float*>(p.wg), *wu = static_cast<const float*>(p.wu),
+              *wd = static_cast<const float*>(p.wd);
+  const int parts = f32_out_parts(f, chunk), dparts = f32_dw_parts(f, chunk);
+  float* outs[3] = {static_cast<float*>(p.dwg), static_cast<float*>(p.dwu), static_cast<float*>(p.dwd)};
   dsa3d_status_t rc;
   for (int64_t r0 = 0; r0 < f.rows; r0 += chunk) {
     const int64_t n = std::min(chunk, f.rows - r0);
-    const T *x = at_row<T>(p.x, r0, f.C), *dy = at_row<T>(p.dy, r0, f.C);
-    AnyArgs a{};
-    a.A[0] = a.A[1] = {x, f.C, 1};
-    a.A[2] = {dy, f.C, 1};
-    a.B[0] = {p.wg, 1, f.hidden};
-    a.B[1] = {p.wu, 1, f.hidden};
-    a.B[2] = {p.wd, f.C, 1};
+    const float *x = at_row<float>(p.x, r0, C), *dy = at_row<float>(p.dy, r0, C);
+    F32Batch b{};
+    F32Args& a = b.p[0];
+    a.A[0] = a.A[1] = {x, C, 1};
+    a.A[2] = {dy, C, 1};
+    a.B[0] = {wg, 1, H};
+    a.B[1] = {wu, 1, H};
+    a.B[2] = {wd, C, 1};
     a.out[0] = dg; a.out[1] = du; a.out[2] = h;
-    a.M = n; a.N = f.hidden; a.K = f.C;
-    a.act = f.act;
-    if ((rc = any_launch<T, kAnyHiddenBwd>(a, 1, st)) != DSA3D_OK) return rc;
-    AnyArgs b{};
-    b.A[0] = {dg, f.hidden, 1};
-    b.A[1] = {du, f.hidden, 1};
-    b.B[0] = {p.wg, f.hidden, 1};
-    b.B[1] = {p.wu, f.hidden, 1};
-    b.out[0] = const_cast<T*>(at_row<T>(p.dx, r0, f.C));
-    b.M = n; b.N = f.C; b.K = f.hidden;
-    b.products = 2;
-    if ((rc = any_launch<T, kAnyOut>(b, 1, st)) != DSA3D_OK) return rc;
+    a.M = n; a.N = H; a.K = C;
+    a.parts = 1; a.act = f.act;
+    if ((rc = f32_launch<kF32HiddenBwd>(b, 1, st)) != DSA3D_OK) return rc;
+    F32Batch o{};
+    o.p[0].A[0] = {dg, H, 1};
+    o.p[0].A[1] = {du, H, 1};
+    o.p[0].B[0] = {wg, H, 1};
+    o.p[0].B[1] = {wu, H, 1};
+    o.p[0].products = 2;
+    rc = f32_out(f, o, n, w.sums, parts, nullptr, at_row<float>(p.dx, r0, C), st);
+    if (rc != DSA3D_OK) return rc;
     // weight gradients, summed over the chunk's tokens and added to the earlier chunks'
-    struct { const T *a, *b; int64_t m, n; } w[3] = {
-        {x, dg, f.C, f.hidden}, {x, du, f.C, f.hidden}, {h, dy, f.hidden, f.C}};
+    const struct { const float *a, *b; int64_t m, n; } v[3] = {{x, dg, C, H}, {x, du, C, H}, {h, dy, H, C}};
+    F32Batch d{};
     for (int i = 0; i < 3; i++) {
-      AnyArgs c{};
-      c.A[0] = {w[i].a, 1, w[i].m};
-      c.B[0] = {w[i].b, 1, w[i].n};
-      c.out[0] = partial + (int64_t)i * splits * wn;
-      c.M = w[i].m; c.N = w[i].n; c.K = n;
-      c.accumulate = r0 > 0;
-      if ((rc = any_launch<T, kAnyPartial>(c, splits, st)) != DSA3D_OK) return rc;
+      F32Args& q = d.p[i];
+      q.A[0] = {v[i].a, 1, v[i].m};
+      q.B[0] = {v[i].b, 1, v[i].n};
+      q.out[0] = w.dw_sums ? w.dw[i] : outs[i];
+      q.M = v[i].m; q.N = v[i].n; q.K = n;
+      q.products = 1; q.parts = dparts;
+      q.accumulate = r0 > 0;
     }
+    if ((rc = f32_launch<kF32Sum>(d, 3, st)) != DSA3D_OK) return rc;
   }
-  void* outs[3] = {p.dwg, p.dwu, p.dwd};
-  for (int i = 0; i < 3; i++)
-    if ((rc = reduce_launch<T>(partial + (int64_t)i * splits * wn, splits, wn, nullptr, outs[i], wn, st)) != DSA3D_OK)
-      return rc;
-  return DSA3D_OK;
+  if (!w.dw_sums) return DSA3D_OK;
+  F32Join r{};
+  for (int i = 0; i < 3; i++) {
+    r.partial[i] = w.dw[i];
+    r.out[i] = outs[i];
+    r.n[i] = C * H;
+  }
+  r.parts = dparts;
+  return f32_join(r, 3, st);
 }
 
 // --- tensor cores -----------------------------------------------------------------------------------
@@ -232,13 +385,13 @@ PFN_cuTensorMapEncodeTiled_v12000 map_encoder() {
   return fn;
 }
 
-// A [rows][cols] bf16 tensor in boxes of box_cols (64: 128-byte swizzle, operands; 32: 64-byte swizzle,
-// results) by box_rows.
-bool matrix_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_cols, int box_rows) {
+// A [rows][cols] bf16 tensor, rows ld elements apart, in boxes of box_cols (64: 128-byte swizzle,
+// operands; 32: 64-byte swizzle, results) by box_rows.
+bool matrix_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_cols, int box_rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 enc = map_encoder();
   if (!enc) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t es[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, es,
@@ -246,35 +399,27 @@ bool matrix_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int b
              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool k_major_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int box_rows) {
-  return matrix_map(m, p, rows, cols, 64, box_rows);
+bool k_major_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+  return matrix_map(m, p, rows, cols, ld, 64, box_rows);
 }
-bool mn_major_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) {
-  return matrix_map(m, p, rows, cols, 64, kFtK);
+bool mn_major_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return matrix_map(m, p, rows, cols, ld, 64, kFtK);
 }
-bool result_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols) { return matrix_map(m, p, rows, cols, 32, 32); }
+bool result_map(CUtensorMap* m, const void* p, int64_t rows, int64_t cols, int64_t ld) {
+  return matrix_map(m, p, rows, cols, ld, 32, 32);
+}
 
-template <int MODE, int CG>
+template <int MODE, int CG, int ACT>
 dsa3d_status_t tc_launch_cg(FtArgs& a, cudaStream_t st) {
   using Cf = FtCfg<MODE, CG>;
-  auto* kern = dsa3d_ffn_tc_kernel<MODE, CG>;
+  auto* kern = dsa3d_ffn_tc_kernel<MODE, CG, ACT>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cf::SMEM) != cudaSuccess)
     return DSA3D_ERR_CUDA;
-  a.tiles = 0;
-  for (int p = 0; p < a.problems; p++) {
-    a.tiles_m[p] = (int)ceil_div(a.M[p], Cf::TILE_M);
-    const int64_t n = a.tiles_m[p] * ceil_div(a.N[p], Cf::TILE_N);
-    if (n > INT_MAX) return DSA3D_ERR_UNSUPPORTED;
-    a.tiles_of[p] = (int)n;
-    a.tiles += n * a.parts;
-  }
-  a.per_part = (int)ceil_div(a.kblocks, a.parts);
-  a.group = 16 / CG;
-  const unsigned grid = (unsigned)(CG * std::min<int64_t>(a.tiles, std::max(1, sm_count() / CG)));
-  return launch(kKernFfnTc, st, [&] {
+  const unsigned grid = (unsigned)(CG * std::min<int64_t>(a.t.units, std::max(1, sm_count() / CG)));
+  return launch(kKernFfnTcHidden + MODE, st, [&] {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kFtThreads);
+    cfg.blockDim = dim3(Cf::THREADS);
     cfg.dynamicSmemBytes = Cf::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -288,103 +433,149 @@ dsa3d_status_t tc_launch_cg(FtArgs& a, cudaStream_t st) {
 }
 template <int MODE>
 dsa3d_status_t tc_launch(FtArgs& a, int cg, cudaStream_t st) {
-  return cg == 2 ? tc_launch_cg<MODE, 2>(a, st) : tc_launch_cg<MODE, 1>(a, st);
+  return cg == 2 ? tc_launch_cg<MODE, 2, 0>(a, st) : tc_launch_cg<MODE, 1, 0>(a, st);
+}
+template <int MODE>
+dsa3d_status_t tc_launch_gated(FtArgs& a, int cg, int act, cudaStream_t st) {
+  if (act == kActSilu)
+    return cg == 2 ? tc_launch_cg<MODE, 2, kActSilu>(a, st) : tc_launch_cg<MODE, 1, kActSilu>(a, st);
+  return cg == 2 ? tc_launch_cg<MODE, 2, kActGelu>(a, st) : tc_launch_cg<MODE, 1, kActGelu>(a, st);
 }
 
-using bf16 = __nv_bfloat16;
+// Copies into 16-byte rows for those of the tensors that need it; a tensor's own pointer otherwise.
+struct Padder {
+  FfnPad a{};
+  int count = 0;
+  const bf16* use(const void* from, bf16* to, int64_t rows, int64_t n, int64_t ld) {
+    const bf16* p = static_cast<const bf16*>(from);
+    if (!to) return p;
+    a.from[count] = p; a.to[count] = to;
+    a.rows[count] = rows; a.n[count] = n; a.ld[count] = ld;
+    count++;
+    return to;
+  }
+  dsa3d_status_t run(cudaStream_t st) {
+    if (count == 0) return DSA3D_OK;
+    int64_t most = 0;
+    for (int i = 0; i < count; i++) most = std::max(most, a.rows[i]);
+    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(most, 8), (int64_t)sm_count() * 8);
+    const int n = count;
+    count = 0;
+    return launch(kKernFfnPad, st, [&] { dsa3d_ffn_pad_kernel<<<dim3(grid, n), 256, 0, st>>>(a); });
+  }
+};
+
+dsa3d_status_t tc_join(const FtTiles& t, int cg, const bf16* add, void* o0, void* o1, void* o2, cudaStream_t st) {
+  FtTail a{};
+  a.t = t;
+  a.add = add;
+  a.out[0] = static_cast<bf16*>(o0);
+  a.out[1] = static_cast<bf16*>(o1);
+  a.out[2] = static_cast<bf16*>(o2);
+  a.tile_m = 128 * cg;
+  int64_t tiles = 0, rows = 0;
+  for (int p = 0; p < t.problems; p++) {
+    tiles += t.tiles_of[p];
+    rows = std::max(rows, std::min<int64_t>(t.M[p], a.tile_m));
+  }
+  // about eight blocks per SM over the tail's tiles, of four rows or more
+  const int64_t tail = tiles - t.full;
+  const unsigned by = (unsigned)std::max<int64_t>(1, std::min(ceil_div(rows, 4), (int64_t)sm_count() * 8 / tail));
+  return launch(kKernFfnReduce, st, [&] { dsa3d_ffn_tail_kernel<<<dim3((unsigned)tail, by), 256, 0, st>>>(a); });
+}
+
+// y or dx: one launch, and the joining of its tail where it has one.
+template <int MODE>
+dsa3d_status_t tc_out(const Ffn& f, FtArgs& a, int64_t n, const float* sums, size_t sums_have, const bf16* add,
+                      bf16* out, cudaStream_t st) {
+  const int cg = tc_pair(n);
+  a.t = tc_out_tiles(f, n, MODE == kTcDx ? 2 : 1);
+  if ((size_t)sums_elems(a.t, cg) > sums_have) {
+    // a last, shorter chunk whose tail would be larger than the others': no cutting
+    a.t.parts = 1;
+    a.t.per_part = a.t.kblocks;
+    a.t.full = f.ldc() != f.C ? 0 : a.t.tiles_of[0];
+    a.t.units = a.t.tiles_of[0];
+  }
+  a.t.sums = const_cast<float*>(sums);
+  a.add = add;
+  if (a.t.full > 0 && !result_map(&a.o[0], out, n, f.C, f.C)) return DSA3D_ERR_CUDA;
+  const dsa3d_status_t rc = tc_launch<MODE>(a, cg, st);
+  if (rc != DSA3D_OK || a.t.units == a.t.full) return rc;
+  return tc_join(a.t, cg, add, out, nullptr, nullptr, st);
+}
 
 dsa3d_status_t tc_forward(const Ffn& f, const FfnFwd& p, int64_t chunk, cudaStream_t st) {
-  const int64_t C = f.C, H = f.hidden;
-  float* partial = reinterpret_cast<float*>(static_cast<char*>(p.ws) + align256((size_t)chunk * H * 2));
-  const int out_parts = tc_out_parts(f, chunk);  // of every chunk, the last and shorter one too
+  const int64_t C = f.C, H = f.hidden, lc = f.ldc(), lh = f.ldh(), lw = f.ldw();
+  const FwdWs w = fwd_ws(f, chunk, p.ws);
+  Padder pad;
+  const bf16 *wg = pad.use(p.wg, w.wg, C, H, lh), *wu = pad.use(p.wu, w.wu, C, H, lh),
+             *wd = pad.use(p.wd, w.wd, H, C, lc);
   dsa3d_status_t rc;
   for (int64_t r0 = 0; r0 < f.rows; r0 += chunk) {
     const int64_t n = std::min(chunk, f.rows - r0);
-    const int cg = tc_pair(n);
+    const bf16* x = pad.use(at_row<bf16>(p.x, r0, C), w.x, n, C, lc);
+    if ((rc = pad.run(st)) != DSA3D_OK) return rc;
     FtArgs a{};
-    if (!k_major_map(&a.a[0], at_row<bf16>(p.x, r0, C), n, C, 128) || !mn_major_map(&a.b[0], p.wg, C, H) ||
-        !mn_major_map(&a.b[1], p.wu, C, H) || !result_map(&a.o[0], p.ws, n, H))
+    if (!k_major_map(&a.a[0], x, n, C, lc, 128) || !mn_major_map(&a.b[0], wg, C, H, lh) ||
+        !mn_major_map(&a.b[1], wu, C, H, lh) || !result_map(&a.o[0], w.h, n, H, lw))
       return DSA3D_ERR_CUDA;
-    a.M[0] = n; a.N[0] = H;
-    a.problems = 1; a.parts = 1; a.act = f.act;
-    a.kblocks = (int)ceil_div(C, kFtK);
-    if ((rc = tc_launch<kTcHidden>(a, cg, st)) != DSA3D_OK) return rc;
+    a.t = tc_hidden_tiles(f, n, 128);
+    if ((rc = tc_launch_gated<kTcHidden>(a, tc_pair(n), f.act, st)) != DSA3D_OK) return rc;
     FtArgs b{};
-    bf16* y = const_cast<bf16*>(at_row<bf16>(p.y, r0, C));
-    const bf16* add = p.add ? at_row<bf16>(p.add, r0, C) : nullptr;
-    if (!k_major_map(&b.a[0], p.ws, n, H, 128) || !mn_major_map(&b.b[0], p.wd, H, C) || !result_map(&b.o[0], y, n, C))
-      return DSA3D_ERR_CUDA;
-    b.M[0] = n; b.N[0] = C;
-    b.problems = 1;
-    b.parts = out_parts;
-    b.kblocks = (int)ceil_div(H, kFtK);
-    b.add = add;
-    if (b.parts > 1) b.partial = partial;
-    if ((rc = tc_launch<kTcOut>(b, cg, st)) != DSA3D_OK) return rc;
-    if (b.parts > 1 && (rc = reduce_launch<bf16>(partial, b.parts, n * C, add, y, n * C, st)) != DSA3D_OK) return rc;
+    if (!k_major_map(&b.a[0], w.h, n, H, lw, 128) || !mn_major_map(&b.b[0], wd, H, C, lc)) return DSA3D_ERR_CUDA;
+    rc = tc_out<kTcOut>(f, b, n, w.sums, w.sums_elems, at_row<bf16>(p.add, r0, C), at_row<bf16>(p.y, r0, C), st);
+    if (rc != DSA3D_OK) return rc;
   }
   return DSA3D_OK;
 }
 
 dsa3d_status_t tc_backward(const Ffn& f, const FfnBwd& p, int64_t chunk, cudaStream_t st) {
-  const int64_t C = f.C, H = f.hidden, wn = C * H;
-  const size_t hb = align256((size_t)chunk * H * 2);
-  char* ws = static_cast<char*>(p.ws);
-  void *dg = ws, *du = ws + hb, *h = ws + 2 * hb;
-  const int parts = tc_dw_parts(f, chunk);
-  const int out_parts = tc_out_parts(f, chunk);
-  const bool whole = parts == 1 && chunk >= f.rows;  // the weight gradients are written once, in bf16
-  float* dw_sum = reinterpret_cast<float*>(ws + 3 * hb);
-  float* dx_sum = reinterpret_cast<float*>(ws + 3 * hb + (whole ? 0 : align256((size_t)parts * 3 * wn * 4)));
+  const int64_t C = f.C, H = f.hidden, lc = f.ldc(), lh = f.ldh(), lw = f.ldw();
+  const BwdWs w = bwd_ws(f, chunk, p.ws);
+  FtTiles dw = tc_dw_tiles(f, chunk, dw_all_tail(f, chunk));  // the same tiles for every chunk
+  dw.sums = w.dw[0];
+  Padder pad;
+  const bf16 *wg = pad.use(p.wg, w.wg, C, H, lh), *wu = pad.use(p.wu, w.wu, C, H, lh),
+             *wd = pad.use(p.wd, w.wd, H, C, lc);
   dsa3d_status_t rc;
+  if ((rc = pad.run(st)) != DSA3D_OK) return rc;
   for (int64_t r0 = 0; r0 < f.rows; r0 += chunk) {
     const int64_t n = std::min(chunk, f.rows - r0);
     const int cg = tc_pair(n);
-    const bf16 *x = at_row<bf16>(p.x, r0, C), *dy = at_row<bf16>(p.dy, r0, C);
-    bf16* dx = const_cast<bf16*>(at_row<bf16>(p.dx, r0, C));
+    const bf16 *x = pad.use(at_row<bf16>(p.x, r0, C), w.x, n, C, lc),
+               *dy = pad.use(at_row<bf16>(p.dy, r0, C), w.dy, n, C, lc);
+    if ((rc = pad.run(st)) != DSA3D_OK) return rc;
     FtArgs a{};
-    if (!k_major_map(&a.a[0], dy, n, C, 128) || !k_major_map(&a.a[1], x, n, C, 128) ||
-        !mn_major_map(&a.b[0], p.wg, C, H) || !mn_major_map(&a.b[1], p.wu, C, H) ||
-        !k_major_map(&a.b[2], p.wd, H, C, 128 / cg) || !result_map(&a.o[0], dg, n, H) ||
-        !result_map(&a.o[1], du, n, H) || !result_map(&a.o[2], h, n, H))
+    if (!k_major_map(&a.a[0], dy, n, C, lc, 128) || !k_major_map(&a.a[1], x, n, C, lc, 128) ||
+        !mn_major_map(&a.b[0], wg, C, H, lh) || !mn_major_map(&a.b[1], wu, C, H, lh) ||
+        !k_major_map(&a.b[2], wd, H, C, lc, 256 / cg) || !result_map(&a.o[0], w.dg, n, H, lw) ||
+        !result_map(&a.o[1], w.du, n, H, lw) || !result_map(&a.o[2], w.h, n, H, lw))
       return DSA3D_ERR_CUDA;
-    a.M[0] = n; a.N[0] = H;
-    a.problems = 1; a.parts = 1; a.act = f.act;
-    a.kblocks = (int)ceil_div(C, kFtK);
-    if ((rc = tc_launch<kTcHiddenBwd>(a, cg, st)) != DSA3D_OK) return rc;
+    a.t = tc_hidden_tiles(f, n, 256);
+    if ((rc = tc_launch_gated<kTcHiddenBwd>(a, cg, f.act, st)) != DSA3D_OK) return rc;
     FtArgs b{};
-    if (!k_major_map(&b.a[0], dg, n, H, 128) || !k_major_map(&b.a[1], du, n, H, 128) ||
-        !k_major_map(&b.b[0], p.wg, C, H, 256 / cg) || !k_major_map(&b.b[1], p.wu, C, H, 256 / cg) ||
-        !result_map(&b.o[0], dx, n, C))
+    if (!k_major_map(&b.a[0], w.dg, n, H, lw, 128) || !k_major_map(&b.a[1], w.du, n, H, lw, 128) ||
+        !k_major_map(&b.b[0], wg, C, H, lh, 256 / cg) || !k_major_map(&b.b[1], wu, C, H, lh, 256 / cg))
       return DSA3D_ERR_CUDA;
-    b.M[0] = n; b.N[0] = C;
-    b.problems = 1;
-    b.parts = out_parts;
-    b.kblocks = (int)ceil_div(H, kFtK);
-    if (b.parts > 1) b.partial = dx_sum;
-    if ((rc = tc_launch<kTcDx>(b, cg, st)) != DSA3D_OK) return rc;
-    if (b.parts > 1 && (rc = reduce_launch<bf16>(dx_sum, b.parts, n * C, nullptr, dx, n * C, st)) != DSA3D_OK) return rc;
-    FtArgs w{};
-    if (!mn_major_map(&w.a[0], x, n, C) || !mn_major_map(&w.a[2], h, n, H) || !mn_major_map(&w.b[0], dg, n, H) ||
-        !mn_major_map(&w.b[1], du, n, H) || !mn_major_map(&w.b[2], dy, n, C) || !result_map(&w.o[0], p.dwg, C, H) ||
-        !result_map(&w.o[1], p.dwu, C, H) || !result_map(&w.o[2], p.dwd, H, C))
+    rc = tc_out<kTcDx>(f, b, n, w.sums, w.sums_elems, nullptr, at_row<bf16>(p.dx, r0, C), st);
+    if (rc != DSA3D_OK) return rc;
+    FtArgs d{};
+    d.t = dw;
+    d.t.kblocks = (int)ceil_div(n, kFtK);
+    d.t.per_part = (int)ceil_div(d.t.kblocks, d.t.parts);  // a short last chunk may leave parts empty
+    d.t.accumulate = r0 > 0;
+    if (!mn_major_map(&d.a[0], x, n, C, lc) || !mn_major_map(&d.a[2], w.h, n, H, lw) ||
+        !mn_major_map(&d.b[0], w.dg, n, H, lw) || !mn_major_map(&d.b[1], w.du, n, H, lw) ||
+        !mn_major_map(&d.b[2], dy, n, C, lc))
       return DSA3D_ERR_CUDA;
-    w.a[1] = w.a[0];
-    w.M[0] = w.M[1] = C; w.N[0] = w.N[1] = H;
-    w.M[2] = H; w.N[2] = C;
-    w.problems = 3;
-    w.kblocks = (int)ceil_div(n, kFtK);
-    w.parts = parts;
-    w.partial = whole ? nullptr : dw_sum;
-    w.accumulate = r0 > 0;
-    if ((rc = tc_launch<kTcDw>(w, 2, st)) != DSA3D_OK) return rc;
+    if (dw.full > 0 && (!result_map(&d.o[0], p.dwg, C, H, H) || !result_map(&d.o[1], p.dwu, C, H, H) ||
+                        !result_map(&d.o[2], p.dwd, H, C, C)))
+      return DSA3D_ERR_CUDA;
+    d.a[1] = d.a[0];
+    if ((rc = tc_launch<kTcDw>(d, 2, st)) != DSA3D_OK) return rc;
   }
-  if (whole) return DSA3D_OK;
-  void* outs[3] = {p.dwg, p.dwu, p.dwd};
-  for (int i = 0; i < 3; i++)
-    if ((rc = reduce_launch<bf16>(dw_sum + (int64_t)i * parts * wn, parts, wn, nullptr, outs[i], wn, st)) != DSA3D_OK)
-      return rc;
-  return DSA3D_OK;
+  return dw.units > dw.full ? tc_join(dw, 2, nullptr, p.dwg, p.dwu, p.dwd, st) : DSA3D_OK;
 }
 
 }  // namespace
@@ -434,9 +625,7 @@ dsa3d_status_t dsa3d_gated_ffn(const void* x, const void* gate_weight, const voi
   const int64_t chunk = fit_chunk(f, workspace_bytes, fwd_bytes);
   if (chunk == 0) return DSA3D_ERR_WORKSPACE_TOO_SMALL;
   const FfnFwd p{x, gate_weight, up_weight, down_weight, add, y, workspace};
-  if (use_tc(f)) return tc_forward(f, p, chunk, stream);
-  if (dtype == DSA3D_F32) return any_forward<float>(f, p, chunk, stream);
-  return any_forward<__nv_bfloat16>(f, p, chunk, stream);
+  return f.f32() ? f32_forward(f, p, chunk, stream) : tc_forward(f, p, chunk, stream);
 }
 
 size_t dsa3d_gated_ffn_backward_workspace_bytes(long long rows, int C, int hidden, dsa3d_dtype_t dtype) {
@@ -481,9 +670,7 @@ dsa3d_status_t dsa3d_gated_ffn_backward(const void* x, const void* gate_weight, 
   const int64_t chunk = fit_chunk(f, workspace_bytes, bwd_bytes);
   if (chunk == 0) return DSA3D_ERR_WORKSPACE_TOO_SMALL;
   const FfnBwd p{x, gate_weight, up_weight, down_weight, dy, dx, dgate_weight, dup_weight, ddown_weight, workspace};
-  if (use_tc(f)) return tc_backward(f, p, chunk, stream);
-  if (dtype == DSA3D_F32) return any_backward<float>(f, p, chunk, stream);
-  return any_backward<__nv_bfloat16>(f, p, chunk, stream);
+  return f.f32() ? f32_backward(f, p, chunk, stream) : tc_backward(f, p, chunk, stream);
 }
 
 }  // extern "C"

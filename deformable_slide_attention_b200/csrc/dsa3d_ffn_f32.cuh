@@ -1,0 +1,216 @@
+// dsa3d_ffn_f32.cuh -- the gated feed-forward block for fp32 tensors, on CUDA cores:
+//
+//   g = x Wg, u = x Wu, h = act(g) u, y = h Wd (+ add)                      (Wg, Wu [C][hidden], Wd [hidden][C])
+//   dh = dy Wd^T, dg = dh u act'(g), du = dh act(g), dx = dg Wg^T + du Wu^T,
+//   dWg = x^T dg, dWu = x^T du, dWd = h^T dy
+//
+// fp32 products stay fp32 here: the tensor cores' tf32 keeps 11 bits of each factor, and sums of split
+// bf16 factors are cut, not rounded, at every step of the accumulator.  The kernel is bound by the fp32
+// FMA pipes (or, at a few hundred tokens, by how many of them the tiles reach).  Tiles of 64 x 64
+// outputs, 16 along the summed axis, 128 threads with 8 x 4 sums each: 32 FMAs for three 16-byte
+// shared-memory reads.  The next 16 are loaded into registers while these are multiplied, and two
+// shared buffers make one barrier per step enough.  The products of one tile that the same outputs
+// need (gate, up and dh) are formed one after another by the same block, and the activation, its
+// derivative and the element-wise products are the epilogue, so g, u and dh never reach memory.
+#pragma once
+
+#include <stdint.h>
+
+#include "dsa3d_vec.cuh"
+
+namespace dsa3d {
+
+constexpr int kActSilu = 0, kActGelu = 1;
+
+// Activation and derivative.  silu: g s(g), s the logistic function; gelu: g Phi(g), Phi the normal
+// distribution (the exact form, with erf).
+__device__ __forceinline__ void f32_act(int act, float g, float& a, float& da) {
+  if (act == kActSilu) {
+    const float s = 1.f / (1.f + expf(-g));
+    a = g * s;
+    da = s * fmaf(g, 1.f - s, 1.f);
+  } else {
+    const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+    a = g * cdf;
+    da = fmaf(g * 0.39894228040143268f, expf(-0.5f * g * g), cdf);
+  }
+}
+
+constexpr int kF32Tile = 64, kF32K = 16, kF32Threads = 128;
+constexpr int kF32Loads = kF32Tile * kF32K / kF32Threads;  // elements of each operand per thread and step
+
+struct F32Operand {  // element (i, k) of an operand at p[i * si + k * sk]
+  const float* p;
+  int64_t si, sk;
+};
+
+struct F32Smem {
+  float a[2][kF32K][kF32Tile + 4], b[2][kF32K][kF32Tile + 4];
+};
+
+// This thread's elements of one step, from the operand into registers ...
+__device__ __forceinline__ void f32_fetch(float (&r)[kF32Loads], const F32Operand& o, int64_t i0, int64_t ni,
+                                          int64_t k0, int64_t k1) {
+#pragma unroll
+  for (int j = 0; j < kF32Loads; j++) {
+    const int e = threadIdx.x + j * kF32Threads;
+    // consecutive threads along the operand's contiguous axis
+    const int i = o.sk == 1 ? e / kF32K : e % kF32Tile;
+    const int k = o.sk == 1 ? e % kF32K : e / kF32Tile;
+    const bool in = i0 + i < ni && k0 + k < k1;
+    r[j] = in ? __ldg(o.p + (i0 + i) * o.si + (k0 + k) * o.sk) : 0.f;
+  }
+}
+// ... and on to shared memory.
+__device__ __forceinline__ void f32_stash(float (&dst)[kF32K][kF32Tile + 4], const float (&r)[kF32Loads],
+                                          const F32Operand& o) {
+#pragma unroll
+  for (int j = 0; j < kF32Loads; j++) {
+    const int e = threadIdx.x + j * kF32Threads;
+    const int i = o.sk == 1 ? e / kF32K : e % kF32Tile;
+    const int k = o.sk == 1 ? e % kF32K : e / kF32Tile;
+    dst[k][i] = r[j];
+  }
+}
+
+// acc += A[m0.., k0..k1) . B[n0.., k0..k1); thread (ty, tx) holds rows 4 ty + {0..3, 32..35}, columns 4 tx..
+__device__ __forceinline__ void f32_product(float (&acc)[8][4], const F32Operand& A, const F32Operand& B,
+                                            int64_t m0, int64_t M, int64_t n0, int64_t N, int64_t k0, int64_t k1,
+                                            F32Smem& sm) {
+  if (k0 >= k1) return;
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  float ra[kF32Loads], rb[kF32Loads];
+  f32_fetch(ra, A, m0, M, k0, k1);
+  f32_fetch(rb, B, n0, N, k0, k1);
+  __syncthreads();  // the buffers' last readers (of an earlier product) are done
+  f32_stash(sm.a[0], ra, A);
+  f32_stash(sm.b[0], rb, B);
+  __syncthreads();
+  int buf = 0;
+  for (int64_t k = k0; k < k1; k += kF32K, buf ^= 1) {
+    const bool more = k + kF32K < k1;
+    if (more) {
+      f32_fetch(ra, A, m0, M, k + kF32K, k1);
+      f32_fetch(rb, B, n0, N, k + kF32K, k1);
+    }
+#pragma unroll
+    for (int kk = 0; kk < kF32K; kk++) {
+      const float4 a0 = *reinterpret_cast<const float4*>(&sm.a[buf][kk][4 * ty]);
+      const float4 a1 = *reinterpret_cast<const float4*>(&sm.a[buf][kk][4 * ty + 32]);
+      const float4 b0 = *reinterpret_cast<const float4*>(&sm.b[buf][kk][4 * tx]);
+      const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const float b[4] = {b0.x, b0.y, b0.z, b0.w};
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+    if (more) {
+      f32_stash(sm.a[buf ^ 1], ra, A);
+      f32_stash(sm.b[buf ^ 1], rb, B);
+    }
+    __syncthreads();
+  }
+}
+
+enum F32Mode {
+  kF32Hidden,     // out[0] = h
+  kF32HiddenBwd,  // out[0] = dg, out[1] = du, out[2] = h
+  kF32Sum         // out[0] = the sum of up to two products (+ add), or this part's share of it
+};
+
+struct F32Args {
+  F32Operand A[3], B[3];  // the products' operands; B's rows are output columns
+  const float* add;       // [M][N] or null
+  float* out[3];          // [M][N]; kF32Sum with parts: [part][M][N]
+  int64_t M, N, K;
+  int products, parts, act;
+  bool accumulate;        // kF32Sum: add to what out[0] holds
+};
+struct F32Batch {  // blockIdx.z picks one
+  F32Args p[3];
+};
+
+template <int MODE>
+__global__ void __launch_bounds__(kF32Threads) dsa3d_ffn_f32_kernel(const __grid_constant__ F32Batch batch) {
+  __shared__ __align__(16) F32Smem sm;
+  const F32Args& g = batch.p[MODE == kF32Sum ? blockIdx.z : 0];
+  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int64_t tiles_n = (g.N + kF32Tile - 1) / kF32Tile;
+  const int64_t m0 = blockIdx.x / tiles_n * kF32Tile, n0 = blockIdx.x % tiles_n * kF32Tile;
+  if (m0 >= g.M) return;  // a batch's other problem has more tiles
+  constexpr int NA = MODE == kF32Hidden ? 2 : (MODE == kF32HiddenBwd ? 3 : 1);
+  float acc[NA][8][4] = {};
+  if (MODE != kF32Sum) {
+#pragma unroll
+    for (int p = 0; p < NA; p++) f32_product(acc[p], g.A[p], g.B[p], m0, g.M, n0, g.N, 0, g.K, sm);
+  } else {
+    const int64_t len = ((g.K + g.parts - 1) / g.parts + kF32K - 1) / kF32K * kF32K;
+    const int64_t k0 = blockIdx.y * len, k1 = k0 + len < g.K ? k0 + len : g.K;
+    for (int p = 0; p < g.products; p++) f32_product(acc[0], g.A[p], g.B[p], m0, g.M, n0, g.N, k0, k1, sm);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int64_t m = m0 + 4 * ty + (i & 3) + 32 * (i >> 2), n = n0 + 4 * tx + j;
+      if (m >= g.M || n >= g.N) continue;
+      const int64_t at = m * g.N + n;
+      if (MODE == kF32Hidden) {
+        float a, da;
+        f32_act(g.act, acc[0][i][j], a, da);
+        g.out[0][at] = a * acc[NA > 1 ? 1 : 0][i][j];
+      } else if (MODE == kF32HiddenBwd) {
+        float a, da;
+        f32_act(g.act, acc[0][i][j], a, da);
+        const float u = acc[NA > 1 ? 1 : 0][i][j], dh = acc[NA > 2 ? 2 : 0][i][j];
+        g.out[0][at] = dh * u * da;
+        g.out[1][at] = dh * a;
+        g.out[2][at] = a * u;
+      } else {
+        float* o = g.out[0] + (int64_t)blockIdx.y * g.M * g.N + at;
+        float v = acc[0][i][j];
+        if (g.add) v += g.add[at];
+        *o = g.accumulate ? *o + v : v;
+      }
+    }
+  }
+}
+
+// out[p][i] = sum_s partial[p][s][i] (+ add), in order of s: joins the parts of split sums.
+// blockIdx.y picks one of up to three outputs.
+struct F32Join {
+  const float* partial[3];  // [parts][n]
+  const float* add;         // [n] or null
+  float* out[3];            // [n]
+  int64_t n[3];
+  int parts;
+};
+__global__ void __launch_bounds__(256) dsa3d_ffn_join_kernel(const __grid_constant__ F32Join r) {
+  const int p = blockIdx.y;
+  const int64_t n = r.n[p], step = (int64_t)gridDim.x * blockDim.x;
+  const float* __restrict__ from = r.partial[p];
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
+    float v = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < r.parts; s++) v += __ldg(from + s * n + i);
+    if (r.add) v += r.add[i];
+    r.out[p][i] = v;
+  }
+}
+
+// Rows of n elements copied into rows of ld (a multiple of 8, so that TMA's 16-byte strides fit):
+// up to four tensors, blockIdx.y picks one.
+struct FfnPad {
+  const __nv_bfloat16* from[4];
+  __nv_bfloat16* to[4];
+  int64_t rows[4], n[4], ld[4];
+};
+__global__ void __launch_bounds__(256) dsa3d_ffn_pad_kernel(const __grid_constant__ FfnPad a) {
+  const int p = blockIdx.y;
+  const int64_t n = a.n[p], ld = a.ld[p];
+  for (int64_t row = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; row < a.rows[p]; row += (int64_t)gridDim.x * 8)
+    for (int64_t c = threadIdx.x % 32; c < n; c += 32) a.to[p][row * ld + c] = a.from[p][row * n + c];
+}
+
+}  // namespace dsa3d

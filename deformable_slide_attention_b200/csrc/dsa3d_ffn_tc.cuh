@@ -1,7 +1,8 @@
 // dsa3d_ffn_tc.cuh -- the gated feed-forward block's products on the tensor cores (bf16, sm_100a):
 //
 //   kTcHidden     h = act(x Wg) * (x Wu)                                one tile: 128 columns of g and of u
-//   kTcHiddenBwd  g, u as above and dh = dy Wd^T, then dg = dh u act'(g), du = dh act(g), h = act(g) u
+//   kTcHiddenBwd  dh = dy Wd^T for 256 columns, then g and u for two halves of 128: dg = dh u act'(g),
+//                 du = dh act(g), h = act(g) u
 //   kTcOut        y = h Wd (+ add), whole or in parts of the summed axis
 //   kTcDx         dx = dg Wg^T + du Wu^T                                one accumulator over both products
 //   kTcDw         dWg = x^T dg, dWu = x^T du, dWd = h^T dy               summed over tokens, whole or in parts
@@ -14,12 +15,14 @@
 // A persistent kernel with one CTA per SM, in pairs (CG = 2, cta_group::2): the pair's tile is 256 rows
 // x 256 columns of products, each CTA holds 128 rows of A and half of B, so each operand byte that
 // crosses from L2 feeds twice the products of a single CTA's tile.  The first warp issues the TMA loads,
-// the second (of the pair's first CTA) the MMAs, eight warps the epilogue: accumulators leave tensor
+// the second (of the pair's first CTA) the MMAs, 8 or 16 warps the epilogue: accumulators leave tensor
 // memory 32 columns at a time, the activation and its derivative are formed in registers in fp32, and
 // the results are rounded once and leave through shared memory by TMA, which also clips them to the
-// tensors' edges.  Tensor memory holds two tiles' accumulators (kTcHiddenBwd: g and u once, dh twice,
-// its next tile's dh product running while the epilogue still reads), so that the epilogue of a tile
-// overlaps the products of the next.
+// tensors' edges.  Tensor memory holds two tiles' accumulators, so that the epilogue of a tile overlaps
+// the products of the next.  kTcHiddenBwd fills it with one tile's (dh, and g and u of one half); its 16
+// warps take all their columns into registers at once, which frees tensor memory within a thousand
+// cycles.  (All its products are 256 columns wide: dh in tiles of 128 read shared memory for A as often
+// as for B and ran at 40% of the rate: 963 us against 690 for four 720p frames at hidden 5464.)
 //
 // The products are bound by the tensor cores (6 or 16 rows C hidden operations against a few bytes per
 // element).  Waits are bounded (dsa3d_tc.cuh); no load is multicast.
@@ -29,15 +32,13 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
-#include "dsa3d_ffn_any.cuh"
+#include "dsa3d_ffn_f32.cuh"
 #include "dsa3d_tc.cuh"
 
 namespace dsa3d {
 
 enum TcMode { kTcHidden, kTcHiddenBwd, kTcOut, kTcDx, kTcDw };
 
-constexpr int kFtEpiWarps = 8;
-constexpr int kFtThreads = 32 * (2 + kFtEpiWarps);
 constexpr int kFtK = 64;                 // summed-axis elements per stage
 constexpr uint32_t kFtABytes = 128 * kFtK * 2;
 constexpr uint32_t kFtOutBox = 32 * 32 * 2;  // an epilogue store: 32 rows x 32 columns of bf16
@@ -46,27 +47,39 @@ template <int MODE, int CG>
 struct FtCfg {
   static constexpr bool kGated = MODE == kTcHidden || MODE == kTcHiddenBwd;
   static constexpr int TILE_M = 128 * CG;
-  static constexpr int TILE_N = kGated ? 128 : 256;  // output columns per tile
+  static constexpr int TILE_N = MODE == kTcHidden ? 128 : 256;  // output columns per tile
+  static constexpr int HALVES = MODE == kTcHiddenBwd ? 2 : 1;   // of a tile, each with its own epilogue
+  static constexpr int EPI_WARPS = MODE == kTcHiddenBwd ? 16 : 8;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr int PRODUCTS = MODE == kTcHiddenBwd ? 3 : (MODE == kTcDx ? 2 : 1);  // steps per k-block
   static constexpr uint32_t B_BYTES = 256 / CG * kFtK * 2;
   static constexpr uint32_t STAGE = kFtABytes + B_BYTES;
-  static constexpr int OUT_BUFS = MODE == kTcHiddenBwd ? 3 : 2;
-  static constexpr uint32_t OUT_BYTES = kFtEpiWarps * OUT_BUFS * kFtOutBox;
+  static constexpr int OUT_BUFS = 2;
+  static constexpr uint32_t OUT_BYTES = EPI_WARPS * OUT_BUFS * kFtOutBox;
   static constexpr int STAGES = CG == 2 ? (MODE == kTcHiddenBwd ? 5 : 6) : (MODE == kTcHiddenBwd ? 3 : 4);
   static constexpr uint32_t SMEM = 1024 + STAGES * STAGE + OUT_BYTES + 256;
+};
+
+// The numbering of tiles over up to three outputs (kTcDw has three, the others one).  Tiles from `full`
+// on are the tail: each is cut into `parts` along the summed axis, and every part writes its fp32 sums
+// to sums[(tile - full) * parts + part] ([rows of a tile][256]) for dsa3d_ffn_tail_kernel to join.  The
+// tail is what the CTAs' last, partly empty round would hold; all tiles, when the results' rows are no
+// multiple of 16 bytes (TMA cannot store them) or sums go on over chunks of tokens.
+struct FtTiles {
+  int64_t M[3], N[3];
+  int tiles_of[3], tiles_m[3];
+  int problems, group;  // group: row tiles walked together
+  int kblocks;          // of one product's summed axis
+  int parts, per_part;  // of a tail tile; k-blocks in each part but the last
+  int64_t full, units;  // whole tiles; units of work: full + parts * tail tiles
+  float* sums;
+  bool accumulate;      // add to what sums holds
 };
 
 struct FtArgs {
   CUtensorMap a[3], b[3], o[3];
   const __nv_bfloat16* add;  // kTcOut
-  float* partial;            // parts of the summed axis: [part][M][N] per problem, instead of o
-  int64_t M[3], N[3];        // outputs' sizes per problem (kTcDw: three problems, else one)
-  int64_t tiles;             // over all problems and parts
-  int tiles_of[3];           // per problem and part
-  int tiles_m[3];
-  int kblocks;               // of one product's summed axis
-  int parts, per_part;       // parts of it, k-blocks in each but the last
-  int problems, act, group;  // group: row tiles walked together
-  bool accumulate;           // add to what partial holds
+  FtTiles t;
 };
 
 // ---- cluster helpers ------------------------------------------------------------------------------
@@ -85,6 +98,17 @@ __device__ __forceinline__ void cluster_sync() {
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t .reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 template <int CG>
@@ -164,31 +188,42 @@ __device__ __forceinline__ void ft_commit(uint32_t bar) {
 
 // ---- tiles ------------------------------------------------------------------------------------------
 struct FtTile {
-  int problem, part, kb0, kb1;
+  int problem, kb0, kb1;
   int64_t m0, n0;
+  float* sums;  // a tail part's, else null
 };
-// Tiles are numbered problem by problem, part by part, in groups of `group` row tiles whose columns
-// are walked together, so that the tiles in flight share their operands in L2.
-template <int MODE, int CG>
-__device__ __forceinline__ FtTile ft_tile(const FtArgs& g, int64_t t) {
-  using C = FtCfg<MODE, CG>;
-  FtTile r;
-  r.problem = 0;
-  if (MODE == kTcDw) {
-    while (r.problem < 2 && t >= (int64_t)g.tiles_of[r.problem] * g.parts) {
-      t -= (int64_t)g.tiles_of[r.problem] * g.parts;
-      r.problem++;
-    }
-  }
-  const int per = g.tiles_of[r.problem], tm = g.tiles_m[r.problem];
-  r.part = (int)(t / per);
-  const int i = (int)(t - (int64_t)r.part * per), tn = per / tm;
+// Position of tile i of its problem: groups of `group` row tiles whose columns are walked together, so
+// that the tiles in flight share their operands in L2.
+__device__ __forceinline__ void ft_place(const FtTiles& g, int64_t tile, int tile_m, int tile_n, int& problem,
+                                         int64_t& m0, int64_t& n0) {
+  problem = 0;
+  while (problem + 1 < g.problems && tile >= g.tiles_of[problem]) tile -= g.tiles_of[problem++];
+  const int i = (int)tile, tm = g.tiles_m[problem], tn = g.tiles_of[problem] / tm;
   const int gi = i / (g.group * tn), in = i - gi * g.group * tn;
   const int rows = min(g.group, tm - gi * g.group);
-  r.m0 = (int64_t)(gi * g.group + in % rows) * C::TILE_M;
-  r.n0 = (int64_t)(in / rows) * C::TILE_N;
-  r.kb0 = r.part * g.per_part;
-  r.kb1 = min(r.kb0 + g.per_part, g.kblocks);
+  m0 = (int64_t)(gi * g.group + in % rows) * tile_m;
+  n0 = (int64_t)(in / rows) * tile_n;
+}
+// Halves of a kTcHiddenBwd tile that lie inside the output.
+__device__ __forceinline__ int ft_halves(const FtTiles& g, int64_t n0) { return n0 + 128 < g.N[0] ? 2 : 1; }
+
+template <int MODE, int CG>
+__device__ __forceinline__ FtTile ft_tile(const FtTiles& g, int64_t unit) {
+  using C = FtCfg<MODE, CG>;
+  FtTile r;
+  int64_t tile = unit;
+  r.kb0 = 0;
+  r.kb1 = g.kblocks;
+  r.sums = nullptr;
+  if (!C::kGated && unit >= g.full) {
+    const int64_t u = unit - g.full;
+    const int part = (int)(u % g.parts);
+    tile = g.full + u / g.parts;
+    r.kb0 = part * g.per_part;
+    r.kb1 = min(r.kb0 + g.per_part, g.kblocks);
+    r.sums = g.sums + u * (C::TILE_M * 256);
+  }
+  ft_place(g, tile, C::TILE_M, C::TILE_N, r.problem, r.m0, r.n0);
   return r;
 }
 
@@ -197,10 +232,40 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ float ft_silu_sig(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+// Activation (and derivative) for results in bf16.  silu: s = 1 / (1 + e^-g).  gelu: the normal
+// distribution from erfc by the Chebyshev fit of Press et al., Numerical Recipes (erfcc), whose
+// relative error is below 1.2e-7 everywhere, so that small values keep their digits too; without
+// branches, and a third of erff's instructions.
+template <int ACT, bool DERIV>
+__device__ __forceinline__ void ft_act(float g, float& a, float& da) {
+  if (ACT == kActSilu) {
+    const float s = __fdividef(1.f, 1.f + __expf(-g));
+    a = g * s;
+    if (DERIV) da = s * fmaf(g, 1.f - s, 1.f);
+  } else {
+    const float z = fabsf(g) * 0.70710678118654752f;
+    const float t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
+    float p = 0.17087277f;
+    p = fmaf(p, t, -0.82215223f);
+    p = fmaf(p, t, 1.48851587f);
+    p = fmaf(p, t, -1.13520398f);
+    p = fmaf(p, t, 0.27886807f);
+    p = fmaf(p, t, -0.18628806f);
+    p = fmaf(p, t, 0.09678418f);
+    p = fmaf(p, t, 0.37409196f);
+    p = fmaf(p, t, 1.00002368f);
+    p = fmaf(p, t, -1.26551223f);
+    const float half_erfc = 0.5f * t * __expf(fmaf(-z, z, p));
+    const float cdf = g > 0.f ? 1.f - half_erfc : half_erfc;
+    a = g * cdf;
+    if (DERIV) da = fmaf(g * 0.39894228040143268f, __expf(-z * z), cdf);
+  }
+}
 
-template <int MODE, int CG>
-__global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __grid_constant__ FtArgs g) {
+// ACT (kTcHidden, kTcHiddenBwd): a constant, so that the epilogue's elements are independent instruction
+// streams; a branch per element on the activation held the chain of each exp and reciprocal open.
+template <int MODE, int CG, int ACT>
+__global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kernel(const __grid_constant__ FtArgs g) {
   using C = FtCfg<MODE, CG>;
   extern __shared__ uint8_t ft_smem_raw[];
   const uint32_t raw = smem_u32(ft_smem_raw), base = (raw + 1023u) & ~1023u;
@@ -212,7 +277,7 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tail + 16 * C::STAGES + 32);
   uint32_t* const tslot = reinterpret_cast<uint32_t*>(tail + 16 * C::STAGES + 40);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
   constexpr int kAccBufs = MODE == kTcHiddenBwd ? 1 : 2;  // of 256 columns that the epilogue releases
@@ -224,7 +289,7 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
     }
     for (int s = 0; s < 2; s++) {
       mbar_init(tfull + 8 * s, 1);
-      mbar_init(tempty + 8 * s, kFtEpiWarps * CG);
+      mbar_init(tempty + 8 * s, C::EPI_WARPS * CG);
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -242,23 +307,30 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
     if (lane == 0) {
       uint32_t it = 0;
       bool ok = true;
-      for (int64_t t = first; ok && t < g.tiles; t += stride) {
-        const FtTile tl = ft_tile<MODE, CG>(g, t);
+      for (int64_t t = first; ok && t < g.t.units; t += stride) {
+        const FtTile tl = ft_tile<MODE, CG>(g.t, t);
         const int m = (int)tl.m0 + (int)rank * 128, n = (int)tl.n0;
-        constexpr int SEGS = (MODE == kTcHiddenBwd || MODE == kTcDx) ? 2 : 1;
-#pragma unroll
-        for (int seg = 0; seg < SEGS; seg++) {
-          const bool dh = MODE == kTcHiddenBwd && seg == 0;
-          const int which = MODE == kTcDw ? tl.problem : seg;
-          const void* ma = &g.a[which];
-          for (int kb = tl.kb0; ok && kb < tl.kb1; kb++, it++) {
+        const int nkb = tl.kb1 - tl.kb0;
+        const int steps = (MODE == kTcHiddenBwd ? 1 + ft_halves(g.t, tl.n0) : C::PRODUCTS) * nkb;
+        for (int i = 0; ok && i < steps; i++, it++) {
+          {
+            // which product: kTcHiddenBwd dh, then g and u of the halves; kTcDx both gradients in turn
+            int seg = 0, kb = tl.kb0 + i;
+            if (C::PRODUCTS > 1)
+              while (kb >= tl.kb0 + nkb) {
+                seg++;
+                kb -= nkb;
+              }
+            const bool dh = MODE == kTcHiddenBwd && seg == 0;
+            const int which = MODE == kTcDw ? tl.problem : min(seg, 1);
+            const void* ma = &g.a[which];
             const int s = it % C::STAGES;
             if (it >= C::STAGES) ok = mbar_wait(empty + 8 * s, (it / C::STAGES - 1) & 1, abort_flag);
             if (!ok) break;
             const uint32_t sa = base + s * C::STAGE, sb = sa + kFtABytes;
             const uint32_t local = full + 8 * s;
             const uint32_t bar = CG == 2 ? map_to_rank(local, 0) : local;
-            if (rank == 0) mbar_arrive_expect_tx(local, CG * kFtABytes + (dh ? 128 : 256) * kFtK * 2);
+            if (rank == 0) mbar_arrive_expect_tx(local, CG * kFtABytes + 256 * kFtK * 2);
             const int k = kb * kFtK;
             if (MODE == kTcDw) {  // MN-major A: two boxes of 64 rows
               ft_tma_load<CG>(sa, ma, bar, m, k);
@@ -267,12 +339,13 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
               ft_tma_load<CG>(sa, ma, bar, k, m);
             }
             if (dh) {  // Wd's rows n.. as B, K-major
-              ft_tma_load<CG>(sb, &g.b[2], bar, k, n + (int)rank * 64);
+              ft_tma_load<CG>(sb, &g.b[2], bar, k, n + (int)rank * 128);
             } else if (C::kGated) {  // Wg's and Wu's columns, MN-major: gate for the first half of B
+              const int c = n + (MODE == kTcHiddenBwd ? 128 * (seg - 1) : 0);
               if (CG == 1) {
-                for (int j = 0; j < 4; j++) ft_tma_load<CG>(sb + 8192 * j, &g.b[j >> 1], bar, n + (j & 1) * 64, k);
+                for (int j = 0; j < 4; j++) ft_tma_load<CG>(sb + 8192 * j, &g.b[j >> 1], bar, c + (j & 1) * 64, k);
               } else {
-                for (int j = 0; j < 2; j++) ft_tma_load<CG>(sb + 8192 * j, &g.b[rank], bar, n + j * 64, k);
+                for (int j = 0; j < 2; j++) ft_tma_load<CG>(sb + 8192 * j, &g.b[rank], bar, c + j * 64, k);
               }
             } else if (MODE == kTcDx) {
               ft_tma_load<CG>(sb, &g.b[seg], bar, k, n + (int)rank * 128);
@@ -291,55 +364,72 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
       }
     }
   } else if (warp == 1) {
-    // ---- MMA issuer: one thread, of the pair's first CTA
-    if (lane == 0 && rank == 0) {
+    // ---- MMA issuer: one warp of the pair's first CTA.  The warp stays converged and only the MMAs and
+    // commits are one lane's: descriptors and barrier addresses then live in uniform registers, which
+    // the instructions take.  (With the whole loop inside one lane's branch a step of four MMAs took
+    // 600 cycles to issue, more than the 512 they run.)
+    if (rank == 0) {
       constexpr uint32_t ID = umma_idesc_bf16(128 * CG, 256, MODE == kTcDw, MODE != kTcDx);
-      constexpr uint32_t ID_DH = umma_idesc_bf16(128 * CG, 128, false, false);
+      constexpr uint32_t ID_DH = umma_idesc_bf16(128 * CG, 256, false, false);
       constexpr uint32_t A_STEP = MODE == kTcDw ? 2048 : 32;  // bytes per 16 of the summed axis
       constexpr uint32_t B_STEP = MODE == kTcDx ? 32 : 2048;
-      uint32_t it = 0, n_tile = 0;
+      const uint64_t da0 = umma_sdesc_sw128(base, MODE == kTcDw ? 8192 : 16, 1024);
+      const uint64_t db0 = umma_sdesc_sw128(base + kFtABytes, MODE == kTcDx ? 16 : 8192, 1024);
+      const uint64_t db0_dh = umma_sdesc_sw128(base + kFtABytes, 16, 1024);
+      uint32_t stage = 0, phase = 0, n_acc = 0;  // n_acc: accumulators handed to the epilogue so far
       bool ok = true;
-      for (int64_t t = first; ok && t < g.tiles; t += stride, n_tile++) {
-        const FtTile tl = ft_tile<MODE, CG>(g, t);
-        const int nkb = tl.kb1 - tl.kb0;
-        const uint32_t buf = kAccBufs == 2 ? (n_tile & 1) : 0;
-        constexpr int SEGS = (MODE == kTcHiddenBwd || MODE == kTcDx) ? 2 : 1;
-#pragma unroll
-        for (int seg = 0; seg < SEGS; seg++) {
-          const bool dh = MODE == kTcHiddenBwd && seg == 0;
-          const uint32_t d = tmem + (dh ? 256 + 128 * (n_tile & 1) : 256 * buf);
-          // the columns' previous tile has been read (dh's: known since the last tile's wait for g, u)
-          if (!dh && (MODE != kTcDx || seg == 0)) {
-            if (n_tile >= (uint32_t)kAccBufs)
-              ok = ok && mbar_wait(tempty + 8 * buf, (n_tile / kAccBufs - 1) & 1, abort_flag);
-          }
-          for (int kb = 0; ok && kb < nkb; kb++, it++) {
-            const int s = it % C::STAGES;
-            ok = mbar_wait(full + 8 * s, (it / C::STAGES) & 1, abort_flag);
+      for (int64_t t = first; ok && t < g.t.units; t += stride) {
+        int nkb, halves;
+        {
+          const FtTile tl = ft_tile<MODE, CG>(g.t, t);
+          nkb = tl.kb1 - tl.kb0;
+          halves = MODE == kTcHiddenBwd ? ft_halves(g.t, tl.n0) : 1;
+        }
+        for (int half = 0; ok && half < halves; half++, n_acc++) {
+          const uint32_t buf = kAccBufs == 2 ? (n_acc & 1) : 0;
+          if (n_acc >= (uint32_t)kAccBufs)  // the columns' previous contents have been read
+            ok = __all_sync(kFull, mbar_wait(tempty + 8 * buf, (n_acc / kAccBufs - 1) & 1, abort_flag));
+          const int dh_steps = (MODE == kTcHiddenBwd && half == 0) ? nkb : 0;
+          const int steps = dh_steps + (MODE == kTcDx ? 2 : 1) * nkb;
+          for (int i = 0; ok && i < steps; i++) {
+            const bool dh = MODE == kTcHiddenBwd && i < dh_steps;
+            ok = __all_sync(kFull, mbar_wait(full + 8 * stage, phase, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t sa = base + s * C::STAGE, sb = sa + kFtABytes;
-            const uint64_t da = umma_sdesc_sw128(sa, MODE == kTcDw ? 8192 : 16, 1024);
-            const uint64_t db = umma_sdesc_sw128(sb, (dh || MODE == kTcDx) ? 16 : 8192, 1024);
+            const uint32_t d = tmem + (dh ? 256 : 256 * buf);
+            const uint64_t da = da0 + (uint64_t)(stage * (C::STAGE >> 4));
+            const uint64_t db = (dh ? db0_dh : db0) + (uint64_t)(stage * (C::STAGE >> 4));
+            const uint32_t more = i != 0 && i != dh_steps;  // a later step of a product adds
+            if (elect_one()) {
+              if (MODE == kTcHiddenBwd && dh) {
 #pragma unroll
-            for (int k = 0; k < kFtK / 16; k++) {
-              const uint32_t acc = (kb > 0 || k > 0 || (MODE == kTcDx && seg > 0)) ? 1u : 0u;
-              ft_mma<CG>(d, da + (uint64_t)(k * A_STEP >> 4), db + (uint64_t)(k * (dh ? 32 : B_STEP) >> 4),
-                         dh ? ID_DH : ID, acc);
+                for (int k = 0; k < kFtK / 16; k++)
+                  ft_mma<CG>(d, da + (uint64_t)(k * A_STEP >> 4), db + (uint64_t)(k * 32 >> 4), ID_DH, k > 0 ? 1u : more);
+              } else {
+#pragma unroll
+                for (int k = 0; k < kFtK / 16; k++)
+                  ft_mma<CG>(d, da + (uint64_t)(k * A_STEP >> 4), db + (uint64_t)(k * B_STEP >> 4), ID, k > 0 ? 1u : more);
+              }
+              ft_commit<CG>(empty + 8 * stage);
             }
-            ft_commit<CG>(empty + 8 * s);
+            __syncwarp();
+            if (++stage == C::STAGES) {
+              stage = 0;
+              phase ^= 1;
+            }
           }
+          if (ok && elect_one()) ft_commit<CG>(tfull + 8 * (n_acc & 1));
+          __syncwarp();
         }
-        if (ok) ft_commit<CG>(tfull + 8 * (n_tile & 1));
       }
     }
   } else {
-    // ---- epilogue: warp e reads tensor-memory lanes 32 (warp % 4).., half the tile's columns
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    // ---- epilogue: a warp reads tensor-memory lanes 32 (warp % 4).., and its share of the columns
+    const int quarter = warp & 3, share = (warp - 2) >> 2;
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
     const uint32_t obuf = out_base + (uint32_t)(warp - 2) * C::OUT_BUFS * kFtOutBox;
     const uint32_t free_bar = CG == 2 ? map_to_rank(tempty, 0) : tempty;
-    uint32_t n_tile = 0, n_store = 0;
+    uint32_t n_acc = 0, n_store = 0;
     // 32 columns of this lane's row into a staging box (64-byte rows, 64-byte swizzle) and out by TMA
     auto put = [&](const void* map, const uint32_t (&v)[16], int col, int row) {
       if (lane == 0) bulk_wait_read<C::OUT_BUFS - 1>();
@@ -357,85 +447,94 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
       __syncwarp();
       if (lane == 0) ft_tma_store(map, box, col, row);
     };
-    for (int64_t t = first; t < g.tiles; t += stride, n_tile++) {
-      const FtTile tl = ft_tile<MODE, CG>(g, t);
-      if (!__all_sync(kFull, mbar_wait(tfull + 8 * (n_tile & 1), (n_tile >> 1) & 1, abort_flag))) break;
+    auto acc_ready = [&]() -> bool {
+      const bool ok = __all_sync(kFull, mbar_wait(tfull + 8 * (n_acc & 1), (n_acc >> 1) & 1, abort_flag));
       tc_fence_after();
-      const uint32_t buf = kAccBufs == 2 ? (n_tile & 1) : 0;
-      const uint32_t acc = tmem + lane_base + 256 * buf;
-      const int64_t M = g.M[tl.problem], N = g.N[tl.problem];
+      return ok;
+    };
+    auto acc_release = [&](uint32_t buf) {  // this warp's loads from tensor memory are complete
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_or_local<CG>(free_bar + 8 * buf);
+    };
+    bool alive = true;
+    for (int64_t t = first; alive && t < g.t.units; t += stride) {
+      const FtTile tl = ft_tile<MODE, CG>(g.t, t);
+      const int64_t M = g.t.M[tl.problem], N = g.t.N[tl.problem];
       const int row0 = (int)tl.m0 + (int)rank * 128 + 32 * quarter;
-      if (C::kGated) {
+      if (MODE == kTcHiddenBwd) {
+        const int halves = ft_halves(g.t, tl.n0);
+        for (int half = 0; half < halves; half++, n_acc++) {
+          if (!acc_ready()) {
+            alive = false;
+            break;
+          }
+          const int col = 32 * share, n = (int)tl.n0 + 128 * half + col;
+          uint32_t gv[32], uv[32], dv[32];
+          tmem_ld32(tmem + lane_base + col, gv);
+          tmem_ld32(tmem + lane_base + 128 + col, uv);
+          tmem_ld32(tmem + lane_base + 256 + 128 * half + col, dv);
+          tmem_ld_wait(gv);
+          tmem_ld_wait(uv);
+          tmem_ld_wait(dv);
+          acc_release(0);
+          if (row0 >= M || n >= N) continue;
+          uint32_t o0[16], o1[16], o2[16];
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            float r0[2], r1[2], r2[2];
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const float gg = __uint_as_float(gv[2 * i + e]), uu = __uint_as_float(uv[2 * i + e]);
+              const float dd = __uint_as_float(dv[2 * i + e]);
+              float a, da;
+              ft_act<ACT, true>(gg, a, da);
+              r0[e] = dd * uu * da;
+              r1[e] = dd * a;
+              r2[e] = a * uu;
+            }
+            o0[i] = pack_bf16(r0[0], r0[1]);
+            o1[i] = pack_bf16(r1[0], r1[1]);
+            o2[i] = pack_bf16(r2[0], r2[1]);
+          }
+          put(&g.o[0], o0, n, row0);
+          put(&g.o[1], o1, n, row0);
+          put(&g.o[2], o2, n, row0);
+        }
+        continue;
+      }
+      if (!acc_ready()) break;
+      const uint32_t buf = n_acc & 1;
+      n_acc++;
+      const uint32_t acc = tmem + lane_base + 256 * buf;
+      if (MODE == kTcHidden) {
 #pragma unroll 1
         for (int c = 0; c < 2; c++) {
-          const int col = half * 64 + c * 32;
+          const int col = share * 64 + c * 32;
           uint32_t gv[32], uv[32], o[16];
           tmem_ld32(acc + col, gv);
           tmem_ld32(acc + 128 + col, uv);
-          const bool in = row0 < M && tl.n0 + col < N;
-          if (MODE == kTcHidden) {
-            tmem_ld_wait(gv);
-            tmem_ld_wait(uv);
-            if (c == 1) {
-              tc_fence_before();
-              if (lane == 0) mbar_arrive_cluster_or_local<CG>(free_bar + 8 * buf);
-            }
-            if (!in) continue;
+          tmem_ld_wait(gv);
+          tmem_ld_wait(uv);
+          if (c == 1) acc_release(buf);
+          if (row0 >= M || tl.n0 + col >= N) continue;
 #pragma unroll
-            for (int i = 0; i < 16; i++) {
-              float h[2];
+          for (int i = 0; i < 16; i++) {
+            float h[2];
 #pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const float gg = __uint_as_float(gv[2 * i + e]), uu = __uint_as_float(uv[2 * i + e]);
-                h[e] = (g.act == kActSilu ? gg * ft_silu_sig(gg) : ffn_act_only<__nv_bfloat16>(kActGelu, gg)) * uu;
-              }
-              o[i] = pack_bf16(h[0], h[1]);
+            for (int e = 0; e < 2; e++) {
+              float a, da;
+              ft_act<ACT, false>(__uint_as_float(gv[2 * i + e]), a, da);
+              h[e] = a * __uint_as_float(uv[2 * i + e]);
             }
-            put(&g.o[0], o, (int)tl.n0 + col, row0);
-          } else {
-            uint32_t dv[32];
-            tmem_ld32(tmem + lane_base + 256 + 128 * (n_tile & 1) + col, dv);
-            tmem_ld_wait(gv);
-            tmem_ld_wait(uv);
-            tmem_ld_wait(dv);
-            if (c == 1) {
-              tc_fence_before();
-              if (lane == 0) mbar_arrive_cluster_or_local<CG>(free_bar);
-            }
-            if (!in) continue;
-            uint32_t o1[16], o2[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) {
-              float r0[2], r1[2], r2[2];
-#pragma unroll
-              for (int e = 0; e < 2; e++) {
-                const float gg = __uint_as_float(gv[2 * i + e]), uu = __uint_as_float(uv[2 * i + e]);
-                const float dd = __uint_as_float(dv[2 * i + e]);
-                float a, da;
-                if (g.act == kActSilu) {
-                  const float s = ft_silu_sig(gg);
-                  a = gg * s;
-                  da = s * fmaf(gg, 1.f - s, 1.f);
-                } else {
-                  ffn_act<__nv_bfloat16>(kActGelu, gg, a, da);
-                }
-                r0[e] = dd * uu * da;
-                r1[e] = dd * a;
-                r2[e] = a * uu;
-              }
-              o[i] = pack_bf16(r0[0], r0[1]);
-              o1[i] = pack_bf16(r1[0], r1[1]);
-              o2[i] = pack_bf16(r2[0], r2[1]);
-            }
-            put(&g.o[0], o, (int)tl.n0 + col, row0);
-            put(&g.o[1], o1, (int)tl.n0 + col, row0);
-            put(&g.o[2], o2, (int)tl.n0 + col, row0);
+            o[i] = pack_bf16(h[0], h[1]);
           }
+          put(&g.o[0], o, (int)tl.n0 + col, row0);
         }
       } else {
 #pragma unroll 1
         for (int c = 0; c < 4; c++) {
-          const int col = half * 128 + c * 32;
+          const int col = share * 128 + c * 32;
           uint32_t v[32];
           tmem_ld32(acc + col, v);
           tmem_ld_wait(v);
@@ -443,28 +542,21 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 32; i++) v[i] = 0u;
           }
-          if (c == 3) {
-            tc_fence_before();
-            if (lane == 0) mbar_arrive_cluster_or_local<CG>(free_bar + 8 * buf);
-          }
+          if (c == 3) acc_release(buf);
           if (row0 >= M || tl.n0 + col >= N) continue;
           const int64_t row = row0 + lane, n = tl.n0 + col;
-          if (g.partial) {
-            int64_t off = 0;
-            for (int p = 0; p < tl.problem; p++) off += g.M[p] * g.N[p] * g.parts;
-            float* to = g.partial + off + ((int64_t)tl.part * M + row) * N + n;
+          if (tl.sums) {
             if (row < M) {
+              float* to = tl.sums + (int64_t)((int)rank * 128 + 32 * quarter + lane) * 256 + col;
 #pragma unroll
               for (int j = 0; j < 8; j++) {
-                if (n + 4 * j < N) {
-                  float4 x = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                         __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
-                  if (g.accumulate) {
-                    const float4 old = *reinterpret_cast<const float4*>(to + 4 * j);
-                    x.x += old.x; x.y += old.y; x.z += old.z; x.w += old.w;
-                  }
-                  *reinterpret_cast<float4*>(to + 4 * j) = x;
+                float4 x = make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                       __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3]));
+                if (g.t.accumulate) {
+                  const float4 old = *reinterpret_cast<const float4*>(to + 4 * j);
+                  x.x += old.x; x.y += old.y; x.z += old.z; x.w += old.w;
                 }
+                *reinterpret_cast<float4*>(to + 4 * j) = x;
               }
             }
           } else {
@@ -498,6 +590,50 @@ __global__ void __launch_bounds__(kFtThreads, 1) dsa3d_ffn_tc_kernel(const __gri
   if (CG == 2) cluster_sync();  // the pair's barriers and tensor memory stay until both are done
   tc_fence_after();
   if (warp == 1) ft_tmem_dealloc<CG>(tmem);
+}
+
+// Joins the parts of the tail's tiles: out = sum of the parts, in order, (+ add), rounded once.  Block:
+// 64 groups of four columns by four rows; blockIdx.x a tail tile, blockIdx.y a share of its rows.
+struct FtTail {
+  FtTiles t;
+  const __nv_bfloat16* add;
+  __nv_bfloat16* out[3];
+  int tile_m;
+};
+__global__ void __launch_bounds__(256) dsa3d_ffn_tail_kernel(const __grid_constant__ FtTail a) {
+  int problem;
+  int64_t m0, n0;
+  ft_place(a.t, a.t.full + blockIdx.x, a.tile_m, 256, problem, m0, n0);
+  const int64_t M = a.t.M[problem], N = a.t.N[problem];
+  const int c = 4 * (threadIdx.x & 63);
+  const int64_t n = n0 + c;
+  if (n >= N) return;
+  const float* from = a.t.sums + (int64_t)blockIdx.x * a.t.parts * a.tile_m * 256 + c;
+  __nv_bfloat16* out = a.out[problem];
+  for (int r = blockIdx.y * 4 + (threadIdx.x >> 6); r < a.tile_m && m0 + r < M; r += gridDim.y * 4) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < a.t.parts; p++) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(from + ((int64_t)p * a.tile_m + r) * 256));
+      v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    const int64_t at = (m0 + r) * N + n;
+    float o[4] = {v.x, v.y, v.z, v.w};
+    if (N % 4 == 0) {
+      if (a.add) {
+        const uint2 x = *reinterpret_cast<const uint2*>(a.add + at);
+        o[0] += __uint_as_float(x.x << 16);
+        o[1] += __uint_as_float(x.x & 0xffff0000u);
+        o[2] += __uint_as_float(x.y << 16);
+        o[3] += __uint_as_float(x.y & 0xffff0000u);
+      }
+      *reinterpret_cast<uint2*>(out + at) = make_uint2(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (n + e < N) out[at + e] = __float2bfloat16_rn(o[e] + (a.add ? __bfloat162float(a.add[at + e]) : 0.f));
+    }
+  }
 }
 
 }  // namespace dsa3d
