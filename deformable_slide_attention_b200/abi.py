@@ -9,6 +9,7 @@ There is no fallback: if the library is missing, or no CUDA device is present, e
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -40,6 +41,8 @@ def library_path() -> str:
 
 def _load():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -584,13 +587,16 @@ def offset_head_backward(x, dw_weight, dw_bias, pw_weight, doffsets, dims, heads
 
 
 # --- the transformer block around the operator -----------------------------------------------------
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _on_stream(ref, stream, inputs):
     """Context of a call's allocations and launches: ref's device, and the given stream where there is
     one (the outputs and workspaces then belong to that stream).  Inputs that another stream owns are
     recorded on it, so that freeing them right after the call is safe."""
     torch = _torch()
     if stream is None:
-        return torch.cuda.device(ref.device)
+        return _NO_CONTEXT if torch.cuda.current_device() == ref.device.index else torch.cuda.device(ref.device)
     if stream.device != ref.device:
         raise ValueError("stream and tensors must be on one device")
     with torch.cuda.device(ref.device):
@@ -603,6 +609,12 @@ def _on_stream(ref, stream, inputs):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _current_stream_handle():
+    """The current stream's handle without building a Stream object: small calls are bound by the host."""
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _rows2d(t, name):
@@ -632,9 +644,9 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, add=None, out=None, want_sta
     with _on_stream(x, stream, (x, add, weight, bias, out)):
         y = torch.empty_like(x) if out is None else out
         h = None if add is None else torch.empty_like(x)
-        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device) if want_stats else None
+        stats = x.new_empty((2, rows), dtype=torch.float32) if want_stats else None
         _check(dsa3d_layer_norm(x.data_ptr(), _ptr(add), _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(h),
-                                _ptr(stats), rows, C, eps, code, _stream_handle(None)), "dsa3d_layer_norm")
+                                _ptr(stats), rows, C, eps, code, _current_stream_handle()), "dsa3d_layer_norm")
     return y, (x if h is None else h), stats
 
 
@@ -659,10 +671,10 @@ def layer_norm_backward(h, weight, stats, dy, add=None, stream=None):
         if weight is not None:
             dw, db = torch.empty_like(weight), torch.empty_like(weight)
             ws_bytes = dsa3d_layer_norm_backward_workspace_bytes(rows, C, code)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=h.device)
+            ws = weight.new_empty(ws_bytes // 4)
         _check(dsa3d_layer_norm_backward(h.data_ptr(), _ptr(weight), stats.data_ptr(), dy.data_ptr(), _ptr(add),
                                          dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), ws_bytes, rows, C, code,
-                                         _stream_handle(None)), "dsa3d_layer_norm_backward")
+                                         _current_stream_handle()), "dsa3d_layer_norm_backward")
     return dx, dw, db
 
 
@@ -702,10 +714,10 @@ def _rotary(call, what, q, k, dims, axes, first, start, step, base, interleaved,
     _on_device(q, k, qo, ko)
     with _on_stream(q, stream, (q, k, qo, ko)):
         if out is None:
-            qo = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            ko = None if k is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            qo = q.new_empty(q.shape)
+            ko = None if k is None else k.new_empty(q.shape)
         _check(call(q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), ldq, ldk, ldqo, ldko, first, rows, *dims,
-                    heads, dh, axes, start, step, base, 1 if interleaved else 0, code, _stream_handle(None)),
+                    heads, dh, axes, start, step, base, 1 if interleaved else 0, code, _current_stream_handle()),
                what)
     return qo, ko
 
@@ -769,7 +781,7 @@ def gated_ffn(x, gate_weight, up_weight, down_weight, activation="silu", add=Non
         ws = _ffn_workspace(workspace, dsa3d_gated_ffn_workspace_bytes(rows, C, hidden, code), x.device)
         _check(dsa3d_gated_ffn(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), down_weight.data_ptr(),
                                _ptr(add), y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), rows, C, hidden,
-                               _ACTIVATIONS[activation], code, _stream_handle(None)), "dsa3d_gated_ffn")
+                               _ACTIVATIONS[activation], code, _current_stream_handle()), "dsa3d_gated_ffn")
     return y
 
 
@@ -790,6 +802,6 @@ def gated_ffn_backward(x, gate_weight, up_weight, down_weight, dy, activation="s
         _check(dsa3d_gated_ffn_backward(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(),
                                         down_weight.data_ptr(), dy.data_ptr(), *(t.data_ptr() for t in grads),
                                         _ptr(ws), 0 if ws is None else ws.numel(), rows, C, hidden,
-                                        _ACTIVATIONS[activation], code, _stream_handle(None)),
+                                        _ACTIVATIONS[activation], code, _current_stream_handle()),
                "dsa3d_gated_ffn_backward")
     return grads

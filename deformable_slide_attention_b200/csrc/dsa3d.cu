@@ -773,7 +773,8 @@ dsa3d_status_t noalloc_scratch(void** out) {
 }  // namespace dsa3d
 
 namespace dsa3d {
-bool ffn_device_check(int* flag);  // dsa3d_ffn.cu
+bool ffn_device_check(int* flag);    // dsa3d_ffn.cu
+bool block_device_check(int* flag);  // dsa3d_block.cu
 }
 using namespace dsa3d;
 
@@ -1042,14 +1043,14 @@ int dsa3d_tc_clk_read(unsigned* host, int n) {
 
 dsa3d_status_t dsa3d_check_device(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return DSA3D_ERR_CUDA;
-  int flag = 0, ffn_flag = 0;
+  int flag = 0, ffn_flag = 0, block_flag = 0;
   if (cudaMemcpyFromSymbol(&flag, g_dsa3d_check, sizeof(int)) != cudaSuccess) return DSA3D_ERR_CUDA;
-  if (!ffn_device_check(&ffn_flag)) return DSA3D_ERR_CUDA;
+  if (!ffn_device_check(&ffn_flag) || !block_device_check(&block_flag)) return DSA3D_ERR_CUDA;
   if (flag) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_dsa3d_check, &zero, sizeof(int)) != cudaSuccess) return DSA3D_ERR_CUDA;
   }
-  return flag || ffn_flag ? DSA3D_ERR_DEVICE_CHECK : DSA3D_OK;
+  return flag || ffn_flag || block_flag ? DSA3D_ERR_DEVICE_CHECK : DSA3D_OK;
 }
 
 }  // extern "C"

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "dsa3d.h"
 #include "dsa3d_host.cuh"
@@ -18,22 +19,29 @@ namespace {
 
 using namespace host;
 
-constexpr int kNormMaxPer = 16;  // vectors per thread
 constexpr int kNormMaxChannels = 16384;
-constexpr int kNormThreads = 256;  // a block's threads where a row takes fewer
 
 // How rows are spread over threads: TX threads per row (a power of two up to 32, else whole warps),
-// PER vectors per thread, TY rows side by side in a block.
+// PER vectors per thread (a power of two), TY rows side by side in a block, R rows in flight per group
+// of TX threads, and the blocks of a launch.
 struct NormPlan {
-  int v, tx, ty, per;
+  int v, tx, ty, per, r, blocks;
+  bool ring;
+  size_t smem;
 };
-NormPlan norm_plan(int C, int vec) {
-  NormPlan p;
+// Two vectors per thread where a row has more than a warp's 32: fewer threads to sum over, and weights
+// that still fit in registers.  odd_per: the same for rows read element by element (30,000 x 1001 fp32:
+// forward 62 us at 8, 66 and more at 2; backward 103 at 4, 110 at 2).
+NormPlan norm_plan(int C, dsa3d_dtype_t dtype, int odd_per) {
+  NormPlan p{};
+  const int vec = dtype == DSA3D_F32 ? 4 : 8;
   p.v = (C % vec == 0) ? vec : 1;
   const int nv = C / p.v;
-  p.per = 1;
-  // up to 512 threads share a row; longer rows give each thread 2, 4, ... vectors
-  while (ceil_div(nv, p.per) > kNormMaxThreads) p.per *= 2;
+  p.per = nv > 32 ? 2 : 1;
+  if (p.v == 1) {  // single elements: rows in flight come from more blocks instead
+    while (p.per < odd_per && nv > 32 * p.per) p.per *= 2;
+  }
+  while (ceil_div(nv, p.per) > (p.per == 2 ? kNormWideThreads : kNormThreads)) p.per *= 2;
   const int need = (int)ceil_div(nv, p.per);
   if (need <= 32) {
     p.tx = 1;
@@ -42,15 +50,58 @@ NormPlan norm_plan(int C, int vec) {
     p.tx = (need + 31) / 32 * 32;
   }
   p.ty = std::max(1, kNormThreads / p.tx);
+  p.r = 1;
+  return p;
+}
+// Blocks: enough to fill the GPU, each then strides over the rest of the rows.
+int norm_blocks(const NormPlan& p, int64_t rows, int per_sm) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(rows, (int64_t)p.ty * p.r), (int64_t)sm_count() * per_sm));
+}
+NormPlan norm_fwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype) {
+  NormPlan p = norm_plan(C, dtype, 8);
+  // two rows in flight per group (720p: 305 against 316 us), if that leaves a block for every SM
+  if (p.per <= 2 && p.tx <= kNormThreads && ceil_div(rows, 2 * (int64_t)p.ty) >= sm_count()) p.r = 2;
+  p.blocks = norm_blocks(p, rows, 8);
+  return p;
+}
+NormPlan norm_bwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype, bool add) {
+  NormPlan p = norm_plan(C, dtype, 4);
+  const int64_t row = (int64_t)C * elem_size(dtype), sms = sm_count();
+  // short rows: steps of up to 8 KB per tensor (2,000,000 x 64 bf16: 141 us at four rows, 163 at one)
+  while (p.per == 1 && p.r < 4 && p.ty * p.r * 2 * row <= 8192 && ceil_div(rows, (int64_t)p.ty * p.r * 2) >= sms) p.r *= 2;
+  // the ring: whole 16-byte rows, more steps than SMs (a block with one step has nothing to run ahead
+  // of), and two blocks on an SM
+  p.smem = (size_t)kRing * (add ? 3 : 2) * p.ty * p.r * row;
+  p.ring = p.v > 1 && p.per <= 2 && p.smem <= 100 * 1024 && ceil_div(rows, (int64_t)p.ty * p.r) > sms;
+  if (!p.ring) p.smem = 0;
+  p.blocks = norm_blocks(p, rows, p.v == 1 ? 4 : 2);
   return p;
 }
 
-// Blocks of a launch over `rows` rows: enough to fill the GPU, each then strides over the rest.
-int norm_blocks(const NormPlan& p, int64_t rows, int r) {
-  const int threads = p.tx * p.ty;
-  const int per_sm = std::max(1, 1024 / threads);
-  const int64_t want = ceil_div(rows, (int64_t)p.ty * r);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(want, (int64_t)sm_count() * per_sm));
+// Calls f with the plan's PER and R (and RING) as constants; V bounds PER (C <= kNormMaxChannels).
+#define DSA3D_NORM_CASE(PER, R, RING)                                                                       \
+  if constexpr (PER <= (V == 1 ? 32 : kNormMaxChannels / (V * kNormThreads)) && (V > 1 || !RING))           \
+    if (p.per == PER && p.r == R && p.ring == RING)                                                         \
+      return f(std::integral_constant<int, PER>(), std::integral_constant<int, R>(), std::integral_constant<bool, RING>());
+template <int V, typename F>
+dsa3d_status_t norm_fwd_dispatch(const NormPlan& p, F&& f) {
+  DSA3D_NORM_CASE(1, 1, false) DSA3D_NORM_CASE(1, 2, false) DSA3D_NORM_CASE(2, 1, false) DSA3D_NORM_CASE(2, 2, false)
+  DSA3D_NORM_CASE(4, 1, false) DSA3D_NORM_CASE(8, 1, false) DSA3D_NORM_CASE(16, 1, false) DSA3D_NORM_CASE(32, 1, false)
+  return DSA3D_ERR_UNSUPPORTED;
+}
+template <int V, typename F>
+dsa3d_status_t norm_bwd_dispatch(const NormPlan& p, F&& f) {
+  DSA3D_NORM_CASE(1, 1, true) DSA3D_NORM_CASE(1, 2, true) DSA3D_NORM_CASE(1, 4, true) DSA3D_NORM_CASE(2, 1, true)
+  DSA3D_NORM_CASE(1, 1, false) DSA3D_NORM_CASE(1, 2, false) DSA3D_NORM_CASE(1, 4, false) DSA3D_NORM_CASE(2, 1, false)
+  DSA3D_NORM_CASE(4, 1, false) DSA3D_NORM_CASE(8, 1, false) DSA3D_NORM_CASE(16, 1, false) DSA3D_NORM_CASE(32, 1, false)
+  return DSA3D_ERR_UNSUPPORTED;
+}
+#undef DSA3D_NORM_CASE
+
+template <typename K>
+bool norm_smem(K* kern, const NormPlan& p) {  // more than the default 48 KB, the static part included
+  return p.smem <= 40 * 1024 ||
+         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem) == cudaSuccess;
 }
 
 struct NormFwd {
@@ -63,13 +114,16 @@ struct NormFwd {
   float eps;
 };
 
-template <typename T, int V, int PER, int R>
-dsa3d_status_t norm_fwd_go(const NormFwd& a, const NormPlan& p, cudaStream_t st) {
-  const int blocks = norm_blocks(p, a.rows, R);
-  return launch(kKernLayerNorm, st, [&] {
-    dsa3d_layer_norm_kernel<T, V, PER, R><<<blocks, p.tx * p.ty, 0, st>>>(
-        static_cast<const T*>(a.x), static_cast<const T*>(a.add), a.w, a.b, static_cast<T*>(a.y),
-        static_cast<T*>(a.h), a.stats, a.rows, a.C, a.eps, p.tx);
+template <typename T, int V>
+dsa3d_status_t norm_fwd(const NormFwd& a, const NormPlan& p, cudaStream_t st) {
+  return norm_fwd_dispatch<V>(p, [&](auto per, auto r, auto) {
+    constexpr int PER = decltype(per)::value, R = decltype(r)::value;
+    auto* kern = a.add ? dsa3d_layer_norm_kernel<T, V, PER, R, true> : dsa3d_layer_norm_kernel<T, V, PER, R, false>;
+    return launch(kKernLayerNorm, st, [&] {
+      kern<<<p.blocks, p.tx * p.ty, 0, st>>>(
+          static_cast<const T*>(a.x), static_cast<const T*>(a.add), a.w, a.b, static_cast<T*>(a.y),
+          static_cast<T*>(a.h), a.stats, a.rows, a.C, a.eps, p.tx, aligned16(a.w) && aligned16(a.b));
+    });
   });
 }
 
@@ -82,45 +136,20 @@ struct NormBwd {
   int C;
 };
 
-template <typename T, int V, int PER, int R>
-dsa3d_status_t norm_bwd_go(const NormBwd& a, const NormPlan& p, int blocks, cudaStream_t st) {
-  return launch(kKernLayerNormBwd, st, [&] {
-    dsa3d_layer_norm_bwd_kernel<T, V, PER, R><<<blocks, p.tx * p.ty, 0, st>>>(
-        static_cast<const T*>(a.h), a.w, a.stats, static_cast<const T*>(a.dy),
-        static_cast<const T*>(a.add), static_cast<T*>(a.dx), a.partial, a.rows, a.C, p.tx);
+template <typename T, int V>
+dsa3d_status_t norm_bwd(const NormBwd& a, const NormPlan& p, cudaStream_t st) {
+  return norm_bwd_dispatch<V>(p, [&](auto per, auto r, auto ring) {
+    constexpr int PER = decltype(per)::value, R = decltype(r)::value;
+    constexpr bool RING = decltype(ring)::value;
+    auto* kern = a.add ? dsa3d_layer_norm_bwd_kernel<T, V, PER, R, true, RING>
+                       : dsa3d_layer_norm_bwd_kernel<T, V, PER, R, false, RING>;
+    if (!norm_smem(kern, p)) return DSA3D_ERR_CUDA;
+    return launch(kKernLayerNormBwd, st, [&] {
+      kern<<<p.blocks, p.tx * p.ty, p.smem, st>>>(
+          static_cast<const T*>(a.h), a.w, a.stats, static_cast<const T*>(a.dy), static_cast<const T*>(a.add),
+          static_cast<T*>(a.dx), a.partial, a.rows, a.C, p.tx, aligned16(a.w));
+    });
   });
-}
-
-// Rows in flight per group: four where a thread holds one vector of each (bytes in flight hide
-// HBM's latency), unless that would leave SMs without a block.
-int norm_rows_in_flight(const NormPlan& p, int64_t rows) {
-  if (p.per > 1) return 1;
-  return ceil_div(rows, (int64_t)p.ty * 4) >= sm_count() ? 4 : 1;
-}
-
-template <typename T, int V>
-dsa3d_status_t norm_fwd(const NormFwd& a, const NormPlan& p, cudaStream_t st) {
-  switch (p.per) {
-    case 1:
-      return norm_rows_in_flight(p, a.rows) == 4 ? norm_fwd_go<T, V, 1, 4>(a, p, st)
-                                                 : norm_fwd_go<T, V, 1, 1>(a, p, st);
-    case 2: return norm_fwd_go<T, V, 2, 1>(a, p, st);
-    case 4: return norm_fwd_go<T, V, 4, 1>(a, p, st);
-    case 8: return norm_fwd_go<T, V, 8, 1>(a, p, st);
-    default: return norm_fwd_go<T, V, 16, 1>(a, p, st);
-  }
-}
-
-template <typename T, int V>
-dsa3d_status_t norm_bwd(const NormBwd& a, const NormPlan& p, int r, int blocks, cudaStream_t st) {
-  switch (p.per) {
-    case 1:
-      return r == 4 ? norm_bwd_go<T, V, 1, 4>(a, p, blocks, st) : norm_bwd_go<T, V, 1, 1>(a, p, blocks, st);
-    case 2: return norm_bwd_go<T, V, 2, 1>(a, p, blocks, st);
-    case 4: return norm_bwd_go<T, V, 4, 1>(a, p, blocks, st);
-    case 8: return norm_bwd_go<T, V, 8, 1>(a, p, blocks, st);
-    default: return norm_bwd_go<T, V, 16, 1>(a, p, blocks, st);
-  }
 }
 
 int norm_vec(dsa3d_dtype_t t) { return t == DSA3D_F32 ? 4 : 8; }
@@ -128,14 +157,14 @@ int norm_vec(dsa3d_dtype_t t) { return t == DSA3D_F32 ? 4 : 8; }
 dsa3d_status_t check_norm_shape(long long rows, int C, dsa3d_dtype_t dtype) {
   if (!known(dtype) || rows < 0 || C < 1) return DSA3D_ERR_INVALID_ARGUMENT;
   if (C > kNormMaxChannels || rows >= (1LL << 31)) return DSA3D_ERR_UNSUPPORTED;
-  // rows that are no multiple of 16 bytes: one element per thread and step
-  if (norm_plan(C, norm_vec(dtype)).per > kNormMaxPer) return DSA3D_ERR_UNSUPPORTED;
+  if (C % norm_vec(dtype) && C > kNormMaxChannels / 2) return DSA3D_ERR_UNSUPPORTED;  // 32 elements per thread
   return DSA3D_OK;
 }
 
+// Rows of partial sums: of the larger launch of the two, with and without an add.
 size_t norm_bwd_ws_bytes(long long rows, int C, dsa3d_dtype_t dtype) {
-  const NormPlan p = norm_plan(C, norm_vec(dtype));
-  return (size_t)norm_blocks(p, rows, norm_rows_in_flight(p, rows)) * 2 * C * sizeof(float);
+  const int blocks = std::max(norm_bwd_plan(rows, C, dtype, false).blocks, norm_bwd_plan(rows, C, dtype, true).blocks);
+  return (size_t)blocks * 2 * C * sizeof(float);
 }
 
 // --- rotary positions ---------------------------------------------------------------------------
@@ -255,6 +284,14 @@ dsa3d_status_t rotary(const void* q, const void* k, void* qo, void* ko, long lon
 }
 
 }  // namespace
+
+// As ffn_device_check (dsa3d_ffn.cu), for this translation unit's record.
+bool block_device_check(int* flag) {
+  if (cudaMemcpyFromSymbol(flag, g_dsa3d_check, sizeof(int)) != cudaSuccess) return false;
+  const int zero = 0;
+  return *flag == 0 || cudaMemcpyToSymbol(g_dsa3d_check, &zero, sizeof(int)) == cudaSuccess;
+}
+
 }  // namespace dsa3d
 
 using namespace dsa3d;
@@ -281,7 +318,7 @@ dsa3d_status_t dsa3d_layer_norm(const void* x, const void* add, const float* wei
   for (int i = 0; i < 4; i++)  // h may be x or add itself: each element is read before it is written
     if (overlap(ins[i], rh) && !(i < 2 && ins[i].lo == rh.lo)) return DSA3D_ERR_INVALID_ARGUMENT;
   const NormFwd a{x, add, weight, bias, y, h, stats, rows, C, eps};
-  const NormPlan p = norm_plan(C, norm_vec(dtype));
+  const NormPlan p = norm_fwd_plan(rows, C, dtype);
   if (dtype == DSA3D_F32) return p.v == 4 ? norm_fwd<float, 4>(a, p, stream) : norm_fwd<float, 1>(a, p, stream);
   return p.v == 8 ? norm_fwd<__nv_bfloat16, 8>(a, p, stream) : norm_fwd<__nv_bfloat16, 1>(a, p, stream);
 }
@@ -330,20 +367,19 @@ dsa3d_status_t dsa3d_layer_norm_backward(const void* h, const float* weight, con
     for (int j = i + 1; j < 4; j++)
       if (overlap(outs[i], outs[j])) return DSA3D_ERR_INVALID_ARGUMENT;
 
-  const NormPlan p = norm_plan(C, norm_vec(dtype));
-  const int r = norm_rows_in_flight(p, rows), blocks = norm_blocks(p, rows, r);
+  const NormPlan p = norm_bwd_plan(rows, C, dtype, add != nullptr);
   float* partial = weight ? static_cast<float*>(workspace) : nullptr;
   const NormBwd a{h, dy, add, weight, stats, dx, partial, rows, C};
   dsa3d_status_t st;
   if (dtype == DSA3D_F32)
-    st = p.v == 4 ? norm_bwd<float, 4>(a, p, r, blocks, stream) : norm_bwd<float, 1>(a, p, r, blocks, stream);
+    st = p.v == 4 ? norm_bwd<float, 4>(a, p, stream) : norm_bwd<float, 1>(a, p, stream);
   else
-    st = p.v == 8 ? norm_bwd<__nv_bfloat16, 8>(a, p, r, blocks, stream)
-                  : norm_bwd<__nv_bfloat16, 1>(a, p, r, blocks, stream);
+    st = p.v == 8 ? norm_bwd<__nv_bfloat16, 8>(a, p, stream)
+                  : norm_bwd<__nv_bfloat16, 1>(a, p, stream);
   if (st != DSA3D_OK || !weight) return st;
   return launch(kKernNormReduce, stream, [&] {
     dsa3d_norm_reduce_kernel<<<(unsigned)ceil_div(2 * (int64_t)C, 32), dim3(32, 32), 0, stream>>>(
-        partial, blocks, C, dweight, dbias);
+        partial, p.blocks, C, dweight, dbias);
   });
 }
 

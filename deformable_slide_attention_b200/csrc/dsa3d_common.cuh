@@ -206,8 +206,8 @@ __device__ __forceinline__ void unpack3(int r, int& a, int& b, int& c) {
 }
 
 // Device-side check record (set by kernels built with DSA3D_DEBUG, read by dsa3d_check_device).
-// Each translation unit that includes this header (dsa3d.cu, dsa3d_ffn.cu) has a record of its own;
-// dsa3d_check_device reads both.
+// Each translation unit that includes this header (dsa3d.cu, dsa3d_ffn.cu, dsa3d_block.cu) has a record
+// of its own; dsa3d_check_device reads them all.
 static __device__ int g_dsa3d_check;
 
 #ifdef DSA3D_DEBUG

@@ -53,10 +53,10 @@ dsa3d_status_t check_ffn_shape(long long rows, int C, int hidden, dsa3d_dtype_t 
 // --- plan: parts of a summed axis, and the workspace -------------------------------------------------
 int64_t tiles_for(int64_t m, int64_t n, int tile_m, int tile_n) { return ceil_div(m, tile_m) * ceil_div(n, tile_n); }
 
-// fp32.  Parts: as many as keep two blocks per SM busy when the tiles alone do not, each of 128 of the
+// fp32.  Parts: as many as keep four blocks per SM busy when the tiles alone do not, each of 128 of the
 // summed axis or more, none empty.
 int f32_parts(int64_t tiles, int64_t len) {
-  const int64_t slots = 2 * sm_count(), steps = ceil_div(len, kF32K);
+  const int64_t slots = 4 * sm_count(), steps = ceil_div(len, kF32K);
   if (tiles >= slots) return 1;
   const int64_t p = std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 8, (int64_t)kFfnMaxParts}));
   return (int)ceil_div(steps, ceil_div(steps, p));

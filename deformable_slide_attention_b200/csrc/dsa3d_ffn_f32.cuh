@@ -6,10 +6,11 @@
 //
 // fp32 products stay fp32 here: the tensor cores' tf32 keeps 11 bits of each factor, and sums of split
 // bf16 factors are cut, not rounded, at every step of the accumulator.  The kernel is bound by the fp32
-// FMA pipes (or, at a few hundred tokens, by how many of them the tiles reach).  Tiles of 64 x 64
-// outputs, 16 along the summed axis, 128 threads with 8 x 4 sums each: 32 FMAs for three 16-byte
-// shared-memory reads.  The next 16 are loaded into registers while these are multiplied, and two
-// shared buffers make one barrier per step enough.  The products of one tile that the same outputs
+// FMA pipes, or, at a few hundred tokens, by how many of them the tiles reach.  Tiles of 64 x 64 outputs,
+// 16 along the summed axis, 256 threads with 4 x 4 sums each (128 threads with 8 x 4 leave a scheduler
+// one warp: 1001 x 258 x 685 took 253 us).  The next 16 are loaded into registers while these are
+// multiplied, by pointers that only move on, and two shared buffers make one barrier per step enough.
+// The products of one tile that the same outputs
 // need (gate, up and dh) are formed one after another by the same block, and the activation, its
 // derivative and the element-wise products are the epilogue, so g, u and dh never reach memory.
 #pragma once
@@ -36,10 +37,10 @@ __device__ __forceinline__ void f32_act(int act, float g, float& a, float& da) {
   }
 }
 
-constexpr int kF32Tile = 64, kF32K = 16, kF32Threads = 128;
+constexpr int kF32Tile = 64, kF32K = 16, kF32Threads = 256;
 constexpr int kF32Loads = kF32Tile * kF32K / kF32Threads;  // elements of each operand per thread and step
 
-struct F32Operand {  // element (i, k) of an operand at p[i * si + k * sk]
+struct F32Operand {  // element (i, k) of an operand at p[i * si + k * sk]; si or sk is 1
   const float* p;
   int64_t si, sk;
 };
@@ -48,66 +49,73 @@ struct F32Smem {
   float a[2][kF32K][kF32Tile + 4], b[2][kF32K][kF32Tile + 4];
 };
 
-// This thread's elements of one step, from the operand into registers ...
-__device__ __forceinline__ void f32_fetch(float (&r)[kF32Loads], const F32Operand& o, int64_t i0, int64_t ni,
-                                          int64_t k0, int64_t k1) {
+// One thread's share of an operand's steps: consecutive threads along the contiguous axis, the j-th
+// element `apart` behind the first; the pointer moves on by 16 of the summed axis per step.
+struct F32Loader {
+  const float* p;
+  int64_t apart, step;
+  int i, k, di, dk;    // position in the tile, and from element to element
+  unsigned inside;     // bit j: element j's row lies inside the operand
+  __device__ __forceinline__ F32Loader(const F32Operand& o, int64_t i0, int64_t ni, int64_t k0) {
+    const bool along_k = o.sk == 1;
+    i = along_k ? threadIdx.x / kF32K : threadIdx.x % kF32Tile;
+    k = along_k ? threadIdx.x % kF32K : threadIdx.x / kF32Tile;
+    di = along_k ? kF32Threads / kF32K : 0;
+    dk = along_k ? 0 : kF32Threads / kF32Tile;
+    apart = di * o.si + dk * o.sk;
+    step = kF32K * o.sk;
+    p = o.p + (i0 + i) * o.si + (k0 + k) * o.sk;
+    inside = 0;
 #pragma unroll
-  for (int j = 0; j < kF32Loads; j++) {
-    const int e = threadIdx.x + j * kF32Threads;
-    // consecutive threads along the operand's contiguous axis
-    const int i = o.sk == 1 ? e / kF32K : e % kF32Tile;
-    const int k = o.sk == 1 ? e % kF32K : e / kF32Tile;
-    const bool in = i0 + i < ni && k0 + k < k1;
-    r[j] = in ? __ldg(o.p + (i0 + i) * o.si + (k0 + k) * o.sk) : 0.f;
+    for (int j = 0; j < kF32Loads; j++) inside |= (i0 + i + j * di < ni ? 1u : 0u) << j;
   }
-}
-// ... and on to shared memory.
-__device__ __forceinline__ void f32_stash(float (&dst)[kF32K][kF32Tile + 4], const float (&r)[kF32Loads],
-                                          const F32Operand& o) {
+  // left: elements of the summed axis from this step on
+  __device__ __forceinline__ void fetch(float (&r)[kF32Loads], int left) {
 #pragma unroll
-  for (int j = 0; j < kF32Loads; j++) {
-    const int e = threadIdx.x + j * kF32Threads;
-    const int i = o.sk == 1 ? e / kF32K : e % kF32Tile;
-    const int k = o.sk == 1 ? e % kF32K : e / kF32Tile;
-    dst[k][i] = r[j];
+    for (int j = 0; j < kF32Loads; j++)
+      r[j] = ((inside >> j) & 1u) && k + j * dk < left ? __ldg(p + j * apart) : 0.f;
+    p += step;
   }
-}
+  __device__ __forceinline__ void stash(float (&dst)[kF32K][kF32Tile + 4], const float (&r)[kF32Loads]) const {
+#pragma unroll
+    for (int j = 0; j < kF32Loads; j++) dst[k + j * dk][i + j * di] = r[j];
+  }
+};
 
-// acc += A[m0.., k0..k1) . B[n0.., k0..k1); thread (ty, tx) holds rows 4 ty + {0..3, 32..35}, columns 4 tx..
-__device__ __forceinline__ void f32_product(float (&acc)[8][4], const F32Operand& A, const F32Operand& B,
-                                            int64_t m0, int64_t M, int64_t n0, int64_t N, int64_t k0, int64_t k1,
-                                            F32Smem& sm) {
+// acc += A[m0.., k0..k1) . B[n0.., k0..k1); thread (ty, tx) holds rows 4 ty.., columns 4 tx..
+__device__ __forceinline__ void f32_product(float (&acc)[4][4], const F32Operand& A, const F32Operand& B, int64_t m0,
+                                            int64_t M, int64_t n0, int64_t N, int64_t k0, int64_t k1, F32Smem& sm) {
   if (k0 >= k1) return;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  F32Loader la(A, m0, M, k0), lb(B, n0, N, k0);
+  int left = (int)(k1 - k0), buf = 0;
   float ra[kF32Loads], rb[kF32Loads];
-  f32_fetch(ra, A, m0, M, k0, k1);
-  f32_fetch(rb, B, n0, N, k0, k1);
+  la.fetch(ra, left);
+  lb.fetch(rb, left);
   __syncthreads();  // the buffers' last readers (of an earlier product) are done
-  f32_stash(sm.a[0], ra, A);
-  f32_stash(sm.b[0], rb, B);
+  la.stash(sm.a[0], ra);
+  lb.stash(sm.b[0], rb);
   __syncthreads();
-  int buf = 0;
-  for (int64_t k = k0; k < k1; k += kF32K, buf ^= 1) {
-    const bool more = k + kF32K < k1;
+  for (; left > 0; left -= kF32K, buf ^= 1) {
+    const bool more = left > kF32K;
     if (more) {
-      f32_fetch(ra, A, m0, M, k + kF32K, k1);
-      f32_fetch(rb, B, n0, N, k + kF32K, k1);
+      la.fetch(ra, left - kF32K);
+      lb.fetch(rb, left - kF32K);
     }
 #pragma unroll
     for (int kk = 0; kk < kF32K; kk++) {
       const float4 a0 = *reinterpret_cast<const float4*>(&sm.a[buf][kk][4 * ty]);
-      const float4 a1 = *reinterpret_cast<const float4*>(&sm.a[buf][kk][4 * ty + 32]);
       const float4 b0 = *reinterpret_cast<const float4*>(&sm.b[buf][kk][4 * tx]);
-      const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const float a[4] = {a0.x, a0.y, a0.z, a0.w};
       const float b[4] = {b0.x, b0.y, b0.z, b0.w};
 #pragma unroll
-      for (int i = 0; i < 8; i++)
+      for (int i = 0; i < 4; i++)
 #pragma unroll
         for (int j = 0; j < 4; j++) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
     }
     if (more) {
-      f32_stash(sm.a[buf ^ 1], ra, A);
-      f32_stash(sm.b[buf ^ 1], rb, B);
+      la.stash(sm.a[buf ^ 1], ra);
+      lb.stash(sm.b[buf ^ 1], rb);
     }
     __syncthreads();
   }
@@ -140,7 +148,7 @@ __global__ void __launch_bounds__(kF32Threads) dsa3d_ffn_f32_kernel(const __grid
   const int64_t m0 = blockIdx.x / tiles_n * kF32Tile, n0 = blockIdx.x % tiles_n * kF32Tile;
   if (m0 >= g.M) return;  // a batch's other problem has more tiles
   constexpr int NA = MODE == kF32Hidden ? 2 : (MODE == kF32HiddenBwd ? 3 : 1);
-  float acc[NA][8][4] = {};
+  float acc[NA][4][4] = {};
   if (MODE != kF32Sum) {
 #pragma unroll
     for (int p = 0; p < NA; p++) f32_product(acc[p], g.A[p], g.B[p], m0, g.M, n0, g.N, 0, g.K, sm);
@@ -150,10 +158,10 @@ __global__ void __launch_bounds__(kF32Threads) dsa3d_ffn_f32_kernel(const __grid
     for (int p = 0; p < g.products; p++) f32_product(acc[0], g.A[p], g.B[p], m0, g.M, n0, g.N, k0, k1, sm);
   }
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
+  for (int i = 0; i < 4; i++) {
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-      const int64_t m = m0 + 4 * ty + (i & 3) + 32 * (i >> 2), n = n0 + 4 * tx + j;
+      const int64_t m = m0 + 4 * ty + i, n = n0 + 4 * tx + j;
       if (m >= g.M || n >= g.N) continue;
       const int64_t at = m * g.N + n;
       if (MODE == kF32Hidden) {

@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -27,12 +28,18 @@ inline Range range_of(const void* p, size_t bytes) {
 }
 inline bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi; }
 
+// Devices this process has asked about; further ones are looked up on every call.
+constexpr int kKnownDevices = 64;
+
+// SMs of the current device (a property that does not change, looked up once per device).
 inline int sm_count() {
+  static std::atomic<int> known[kKnownDevices];
   int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 1;
-  return sms > 0 ? sms : 1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+  if (dev < kKnownDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return 1;
+  if (dev < kKnownDevices) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
