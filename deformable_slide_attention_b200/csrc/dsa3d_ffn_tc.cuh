@@ -19,9 +19,9 @@
 // memory 32 columns at a time, the activation and its derivative are formed in registers in fp32, and
 // the results are rounded once and leave through shared memory by TMA, which also clips them to the
 // tensors' edges.  Tensor memory holds two tiles' accumulators, so that the epilogue of a tile overlaps
-// the products of the next.  kTcHiddenBwd fills it with one tile's (dh, and g and u of one half); its 16
-// warps take all their columns into registers at once, which frees tensor memory within a thousand
-// cycles.  (All its products are 256 columns wide: dh in tiles of 128 read shared memory for A as often
+// the products of the next.  kTcHiddenBwd fills it with one tile's (dh, and g and u of one half): its 16
+// warps take g and u into registers at once, so that the next half's can start, and a tile's dh follows
+// its first half's g and u, so that the columns of dh are not waited for.  (All its products are 256 columns wide: dh in tiles of 128 read shared memory for A as often
 // as for B and ran at 40% of the rate: 963 us against 690 for four 720p frames at hidden 5464.)
 //
 // The products are bound by the tensor cores (6 or 16 rows C hidden operations against a few bytes per
@@ -31,6 +31,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+
+#include <climits>
 
 #include "dsa3d_ffn_f32.cuh"
 #include "dsa3d_tc.cuh"
@@ -232,33 +234,80 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Activation (and derivative) for results in bf16.  silu: s = 1 / (1 + e^-g).  gelu: the normal
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack_bf16(a, b);
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
+  return pack2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ void bits_of(uint64_t v, uint32_t& a, uint32_t& b) {
+  float x, y;
+  unpack2(v, x, y);
+  a = __float_as_uint(x);
+  b = __float_as_uint(y);
+}
+// Waits for the loads so far, the loaded registers tied to the wait.
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+      :
+      : "memory");
+}
+__device__ __forceinline__ uint64_t both(float v) { return pack2(v, v); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t ex2_both(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(ex2_approx(a), ex2_approx(b));
+}
+__device__ __forceinline__ uint64_t rcp_both(uint64_t v) {
+  float a, b;
+  unpack2(v, a, b);
+  return pack2(rcp_approx(a), rcp_approx(b));
+}
+
+// Activation (and derivative) of two values, for results in bf16: packed pairs halve the issue slots,
+// after which the exponentials and reciprocals bind.  silu: s = 1 / (1 + e^-g).  gelu: the normal
 // distribution from erfc by the Chebyshev fit of Press et al., Numerical Recipes (erfcc), whose
-// relative error is below 1.2e-7 everywhere, so that small values keep their digits too; without
-// branches, and a third of erff's instructions.
+// relative error is below 1.2e-7 everywhere, so that small values keep their digits too; no branches.
 template <int ACT, bool DERIV>
-__device__ __forceinline__ void ft_act(float g, float& a, float& da) {
+__device__ __forceinline__ void ft_act(uint64_t g, uint64_t& a, uint64_t& da) {
+  const uint64_t one = both(1.f);
   if (ACT == kActSilu) {
-    const float s = __fdividef(1.f, 1.f + __expf(-g));
-    a = g * s;
-    if (DERIV) da = s * fmaf(g, 1.f - s, 1.f);
+    const uint64_t s = rcp_both(add2(one, ex2_both(mul2(g, both(-kLog2e)))));
+    a = mul2(g, s);
+    if (DERIV) da = mul2(s, fma2(g, fma2(s, both(-1.f), one), one));
   } else {
-    const float z = fabsf(g) * 0.70710678118654752f;
-    const float t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
-    float p = 0.17087277f;
-    p = fmaf(p, t, -0.82215223f);
-    p = fmaf(p, t, 1.48851587f);
-    p = fmaf(p, t, -1.13520398f);
-    p = fmaf(p, t, 0.27886807f);
-    p = fmaf(p, t, -0.18628806f);
-    p = fmaf(p, t, 0.09678418f);
-    p = fmaf(p, t, 0.37409196f);
-    p = fmaf(p, t, 1.00002368f);
-    p = fmaf(p, t, -1.26551223f);
-    const float half_erfc = 0.5f * t * __expf(fmaf(-z, z, p));
-    const float cdf = g > 0.f ? 1.f - half_erfc : half_erfc;
-    a = g * cdf;
-    if (DERIV) da = fmaf(g * 0.39894228040143268f, __expf(-z * z), cdf);
+    float g0, g1;
+    unpack2(g, g0, g1);
+    const uint64_t z = pack2(fabsf(g0) * 0.70710678118654752f, fabsf(g1) * 0.70710678118654752f);
+    const uint64_t t = rcp_both(fma2(z, both(0.5f), one));
+    uint64_t p = both(0.17087277f);
+    p = fma2(p, t, both(-0.82215223f));
+    p = fma2(p, t, both(1.48851587f));
+    p = fma2(p, t, both(-1.13520398f));
+    p = fma2(p, t, both(0.27886807f));
+    p = fma2(p, t, both(-0.18628806f));
+    p = fma2(p, t, both(0.09678418f));
+    p = fma2(p, t, both(0.37409196f));
+    p = fma2(p, t, both(1.00002368f));
+    p = fma2(p, t, both(-1.26551223f));
+    const uint64_t mzz = mul2(mul2(z, both(-1.f)), z);
+    const uint64_t half_erfc = mul2(mul2(t, both(0.5f)), ex2_both(mul2(add2(mzz, p), both(kLog2e))));
+    float h0, h1, c0, c1;  // of |g|'s upper tail: the distribution is 1 - it for positive g
+    unpack2(half_erfc, h0, h1);
+    unpack2(fma2(half_erfc, both(-1.f), one), c0, c1);
+    const uint64_t cdf = pack2(g0 > 0.f ? c0 : h0, g1 > 0.f ? c1 : h1);
+    a = mul2(g, cdf);
+    if (DERIV) da = fma2(mul2(g, both(0.39894228040143268f)), ex2_both(mul2(mzz, both(kLog2e))), cdf);
   }
 }
 
@@ -280,7 +329,6 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
   const int warp = __shfl_sync(kFull, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
   const int64_t first = blockIdx.x / CG, stride = gridDim.x / CG;
-  constexpr int kAccBufs = MODE == kTcHiddenBwd ? 1 : 2;  // of 256 columns that the epilogue releases
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; s++) {
@@ -289,7 +337,7 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
     }
     for (int s = 0; s < 2; s++) {
       mbar_init(tfull + 8 * s, 1);
-      mbar_init(tempty + 8 * s, C::EPI_WARPS * CG);
+      mbar_init(tempty + 8 * s, C::EPI_WARPS * CG);  // kTcHiddenBwd: [0] g and u, [1] dh
     }
     *abort_flag = 0;
     mbar_fence_init();
@@ -314,15 +362,16 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
         const int steps = (MODE == kTcHiddenBwd ? 1 + ft_halves(g.t, tl.n0) : C::PRODUCTS) * nkb;
         for (int i = 0; ok && i < steps; i++, it++) {
           {
-            // which product: kTcHiddenBwd dh, then g and u of the halves; kTcDx both gradients in turn
+            // which product: kTcHiddenBwd g and u of the first half, dh, g and u of the second; kTcDx both
+            // gradients in turn
             int seg = 0, kb = tl.kb0 + i;
             if (C::PRODUCTS > 1)
               while (kb >= tl.kb0 + nkb) {
                 seg++;
                 kb -= nkb;
               }
-            const bool dh = MODE == kTcHiddenBwd && seg == 0;
-            const int which = MODE == kTcDw ? tl.problem : min(seg, 1);
+            const bool dh = MODE == kTcHiddenBwd && seg == 1;
+            const int which = MODE == kTcDw ? tl.problem : (MODE == kTcHiddenBwd ? (dh ? 0 : 1) : seg);
             const void* ma = &g.a[which];
             const int s = it % C::STAGES;
             if (it >= C::STAGES) ok = mbar_wait(empty + 8 * s, (it / C::STAGES - 1) & 1, abort_flag);
@@ -341,7 +390,7 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
             if (dh) {  // Wd's rows n.. as B, K-major
               ft_tma_load<CG>(sb, &g.b[2], bar, k, n + (int)rank * 128);
             } else if (C::kGated) {  // Wg's and Wu's columns, MN-major: gate for the first half of B
-              const int c = n + (MODE == kTcHiddenBwd ? 128 * (seg - 1) : 0);
+              const int c = n + (MODE == kTcHiddenBwd ? 64 * seg : 0);
               if (CG == 1) {
                 for (int j = 0; j < 4; j++) ft_tma_load<CG>(sb + 8192 * j, &g.b[j >> 1], bar, c + (j & 1) * 64, k);
               } else {
@@ -376,9 +425,10 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
       const uint64_t da0 = umma_sdesc_sw128(base, MODE == kTcDw ? 8192 : 16, 1024);
       const uint64_t db0 = umma_sdesc_sw128(base + kFtABytes, MODE == kTcDx ? 16 : 8192, 1024);
       const uint64_t db0_dh = umma_sdesc_sw128(base + kFtABytes, 16, 1024);
-      uint32_t stage = 0, phase = 0, n_acc = 0;  // n_acc: accumulators handed to the epilogue so far
+      constexpr uint32_t kAccBufs = MODE == kTcHiddenBwd ? 1 : 2;  // of 256 columns
+      uint32_t stage = 0, phase = 0, n_tile = 0, n_acc = 0;  // n_acc: accumulators handed to the epilogue so far
       bool ok = true;
-      for (int64_t t = first; ok && t < g.t.units; t += stride) {
+      for (int64_t t = first; ok && t < g.t.units; t += stride, n_tile++) {
         int nkb, halves;
         {
           const FtTile tl = ft_tile<MODE, CG>(g.t, t);
@@ -386,20 +436,25 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
           halves = MODE == kTcHiddenBwd ? ft_halves(g.t, tl.n0) : 1;
         }
         for (int half = 0; ok && half < halves; half++, n_acc++) {
-          const uint32_t buf = kAccBufs == 2 ? (n_acc & 1) : 0;
-          if (n_acc >= (uint32_t)kAccBufs)  // the columns' previous contents have been read
+          const uint32_t buf = MODE == kTcHiddenBwd ? 0 : (n_acc & 1);
+          // the columns' previous contents have been read
+          if (n_acc >= kAccBufs)
             ok = __all_sync(kFull, mbar_wait(tempty + 8 * buf, (n_acc / kAccBufs - 1) & 1, abort_flag));
-          const int dh_steps = (MODE == kTcHiddenBwd && half == 0) ? nkb : 0;
-          const int steps = dh_steps + (MODE == kTcDx ? 2 : 1) * nkb;
+          const int dh_from = (MODE == kTcHiddenBwd && half == 0) ? nkb : INT_MAX;  // dh's steps follow g and u's
+          const int steps = (MODE == kTcDx || (MODE == kTcHiddenBwd && half == 0) ? 2 : 1) * nkb;
           for (int i = 0; ok && i < steps; i++) {
-            const bool dh = MODE == kTcHiddenBwd && i < dh_steps;
+            const bool dh = MODE == kTcHiddenBwd && i >= dh_from;
+            if (MODE == kTcHiddenBwd && i == dh_from && n_tile > 0) {
+              ok = __all_sync(kFull, mbar_wait(tempty + 8, (n_tile - 1) & 1, abort_flag));
+              if (!ok) break;
+            }
             ok = __all_sync(kFull, mbar_wait(full + 8 * stage, phase, abort_flag));
             if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem + (dh ? 256 : 256 * buf);
             const uint64_t da = da0 + (uint64_t)(stage * (C::STAGE >> 4));
             const uint64_t db = (dh ? db0_dh : db0) + (uint64_t)(stage * (C::STAGE >> 4));
-            const uint32_t more = i != 0 && i != dh_steps;  // a later step of a product adds
+            const uint32_t more = i != 0 && i != dh_from;  // a later step of a product adds
             if (elect_one()) {
               if (MODE == kTcHiddenBwd && dh) {
 #pragma unroll
@@ -470,36 +525,44 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
             break;
           }
           const int col = 32 * share, n = (int)tl.n0 + 128 * half + col;
-          uint32_t gv[32], uv[32], dv[32];
-          tmem_ld32(tmem + lane_base + col, gv);
-          tmem_ld32(tmem + lane_base + 128 + col, uv);
-          tmem_ld32(tmem + lane_base + 256 + 128 * half + col, dv);
+          const uint32_t at = tmem + lane_base + col;
+          // g and u leave tensor memory at once (the next products wait for their columns); what they
+          // give takes their registers' place, and dh is read 16 columns at a time after that
+          uint32_t gv[32], uv[32], o[16], o1[16];
+          tmem_ld32(at, gv);
+          tmem_ld32(at + 128, uv);
           tmem_ld_wait(gv);
           tmem_ld_wait(uv);
-          tmem_ld_wait(dv);
           acc_release(0);
-          if (row0 >= M || n >= N) continue;
-          uint32_t o0[16], o1[16], o2[16];
+          const bool in = row0 < M && n < N;
 #pragma unroll
           for (int i = 0; i < 16; i++) {
-            float r0[2], r1[2], r2[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              const float gg = __uint_as_float(gv[2 * i + e]), uu = __uint_as_float(uv[2 * i + e]);
-              const float dd = __uint_as_float(dv[2 * i + e]);
-              float a, da;
-              ft_act<ACT, true>(gg, a, da);
-              r0[e] = dd * uu * da;
-              r1[e] = dd * a;
-              r2[e] = a * uu;
-            }
-            o0[i] = pack_bf16(r0[0], r0[1]);
-            o1[i] = pack_bf16(r1[0], r1[1]);
-            o2[i] = pack_bf16(r2[0], r2[1]);
+            const uint64_t uu = pair_of(uv[2 * i], uv[2 * i + 1]);
+            uint64_t a, da;
+            ft_act<ACT, true>(pair_of(gv[2 * i], gv[2 * i + 1]), a, da);
+            bits_of(mul2(uu, da), gv[2 * i], gv[2 * i + 1]);
+            bits_of(a, uv[2 * i], uv[2 * i + 1]);
+            o[i] = pack_bf16(mul2(a, uu));
           }
-          put(&g.o[0], o0, n, row0);
-          put(&g.o[1], o1, n, row0);
-          put(&g.o[2], o2, n, row0);
+          if (in) put(&g.o[2], o, n, row0);
+#pragma unroll
+          for (int c = 0; c < 2; c++) {
+            uint32_t dv[16];
+            tmem_ld16(at + 256 + 128 * half + 16 * c, dv);
+            tmem_ld_wait16(dv);
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const uint64_t dd = pair_of(dv[2 * i], dv[2 * i + 1]);
+              const int j = 8 * c + i;
+              o[j] = pack_bf16(mul2(dd, pair_of(gv[2 * j], gv[2 * j + 1])));
+              o1[j] = pack_bf16(mul2(dd, pair_of(uv[2 * j], uv[2 * j + 1])));
+            }
+          }
+          if (half + 1 == halves) acc_release(1);
+          if (in) {
+            put(&g.o[0], o, n, row0);
+            put(&g.o[1], o1, n, row0);
+          }
         }
         continue;
       }
@@ -520,14 +583,9 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
           if (row0 >= M || tl.n0 + col >= N) continue;
 #pragma unroll
           for (int i = 0; i < 16; i++) {
-            float h[2];
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-              float a, da;
-              ft_act<ACT, false>(__uint_as_float(gv[2 * i + e]), a, da);
-              h[e] = a * __uint_as_float(uv[2 * i + e]);
-            }
-            o[i] = pack_bf16(h[0], h[1]);
+            uint64_t a, da;
+            ft_act<ACT, false>(pair_of(gv[2 * i], gv[2 * i + 1]), a, da);
+            o[i] = pack_bf16(mul2(a, pair_of(uv[2 * i], uv[2 * i + 1])));
           }
           put(&g.o[0], o, (int)tl.n0 + col, row0);
         }

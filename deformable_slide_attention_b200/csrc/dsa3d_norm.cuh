@@ -62,14 +62,6 @@ __device__ __forceinline__ void group_sum(float (&v)[R], int TX, float (*buf)[R]
 }
 
 // ---- fp32 vectors in packed pairs: one instruction for two sums or products (V = 1: plain ones) ------
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
 template <int V>
 struct F32s {
   uint64_t p[V / 2];
@@ -89,7 +81,7 @@ struct F32s {
   __device__ __forceinline__ float total() const {
     uint64_t t = p[0];
 #pragma unroll
-    for (int i = 1; i < V / 2; i++) asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(t), "l"(p[i]));
+    for (int i = 1; i < V / 2; i++) t = add2(t, p[i]);
     float a, b;
     unpack2(t, a, b);
     return a + b;
@@ -107,22 +99,21 @@ template <int V>
 __device__ __forceinline__ F32s<V> padd(const F32s<V>& a, const F32s<V>& b) {
   F32s<V> r;
 #pragma unroll
-  for (int i = 0; i < V / 2; i++) asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.p[i]) : "l"(a.p[i]), "l"(b.p[i]));
+  for (int i = 0; i < V / 2; i++) r.p[i] = add2(a.p[i], b.p[i]);
   return r;
 }
 template <int V>
 __device__ __forceinline__ F32s<V> pmul(const F32s<V>& a, const F32s<V>& b) {
   F32s<V> r;
 #pragma unroll
-  for (int i = 0; i < V / 2; i++) asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.p[i]) : "l"(a.p[i]), "l"(b.p[i]));
+  for (int i = 0; i < V / 2; i++) r.p[i] = mul2(a.p[i], b.p[i]);
   return r;
 }
 template <int V>
 __device__ __forceinline__ F32s<V> pfma(const F32s<V>& a, const F32s<V>& b, const F32s<V>& c) {
   F32s<V> r;
 #pragma unroll
-  for (int i = 0; i < V / 2; i++)
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.p[i]) : "l"(a.p[i]), "l"(b.p[i]), "l"(c.p[i]));
+  for (int i = 0; i < V / 2; i++) r.p[i] = fma2(a.p[i], b.p[i], c.p[i]);
   return r;
 }
 template <>
