@@ -1,7 +1,7 @@
 // dsa3d_ffn.cu -- C ABI of the gated feed-forward block (include/dsa3d.h): argument validation, the
 // plan of a call (tokens per chunk, splits, workspace) and the launches.  The kernels are in
-// dsa3d_ffn_tc.cuh (bf16, tensor cores) and dsa3d_ffn_f32.cuh (fp32, CUDA cores; and the joining of
-// split sums).  This file allocates no device memory.
+// dsa3d_ffn_tc.cuh (bf16, tensor cores), dsa3d_ffn_f32.cuh (fp32, CUDA cores) and dsa3d_ffn_rows.cuh (a
+// forward of a few tokens).  This file allocates no device memory.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -13,6 +13,7 @@
 
 #include "dsa3d.h"
 #include "dsa3d_ffn_f32.cuh"
+#include "dsa3d_ffn_rows.cuh"
 #include "dsa3d_ffn_tc.cuh"
 #include "dsa3d_host.cuh"
 
@@ -146,15 +147,37 @@ struct Carver {
   }
 };
 
+// A forward of so few tokens that the weights' bytes bind, with rows of whole 16-byte vectors.  C 4096,
+// hidden 10,944: bf16, one token 62 us against 70 through the tensor-core tiles, two 99 against 70; fp32,
+// four tokens 137 us against 987 through the tiles of 64.
+bool few_rows(const Ffn& f) {
+  const int v = f.f32() ? 4 : 8;
+  return f.rows <= (f.f32() ? kRowsMaxF32 : kRowsMaxBf16) && f.C % v == 0 && f.hidden % v == 0;
+}
+// Parts of a summed axis of K for strips over N columns: two blocks per SM, at least 64 of K in each.
+int rows_parts(const Ffn& f, int K, int N) {
+  const int64_t strips = ceil_div(N, 32 * (f.f32() ? 4 : 8));
+  const int64_t want = std::max<int64_t>({ceil_div(2 * sm_count(), strips), ceil_div(K, kRowsPart), (int64_t)1});
+  const int64_t most = std::max<int64_t>({ceil_div(K, 64), ceil_div(K, kRowsPart), (int64_t)1});
+  return (int)std::min(want, most);
+}
+
 struct FwdWs {
-  char* h;                     // [chunk][ldw]
+  char* h;                     // [chunk][ldw]; of few rows: y's parts (and sums: g's and u's)
   bf16 *x, *wg, *wu, *wd;      // copies with 16-byte rows, where the tensors have none
   float* sums;                 // y's split sums: fp32 [parts][chunk][C], bf16 the tail's tiles
   size_t sums_elems, bytes;
 };
 FwdWs fwd_ws(const Ffn& f, int64_t chunk, void* base) {
   Carver c{static_cast<char*>(base)};
-  FwdWs w;
+  FwdWs w{};
+  if (few_rows(f)) {
+    w.sums_elems = (size_t)rows_parts(f, f.C, f.hidden) * 2 * f.rows * f.hidden;
+    w.sums = c.take<float>(true, w.sums_elems);
+    w.h = c.take<char>(true, (size_t)rows_parts(f, f.hidden, f.C) * f.rows * f.C * sizeof(float));
+    w.bytes = c.used;
+    return w;
+  }
   const bool padc = f.ldc() != f.C, padh = f.ldh() != f.hidden;
   w.h = c.take<char>(true, (size_t)chunk * f.ldw() * f.es());
   w.x = c.take<bf16>(padc, (size_t)chunk * f.ldc());
@@ -368,6 +391,51 @@ dsa3d_status_t f32_backward(const Ffn& f, const FfnBwd& p, int64_t chunk, cudaSt
   }
   r.parts = dparts;
   return f32_join(r, 3, st);
+}
+
+// --- a few tokens -----------------------------------------------------------------------------------
+template <typename T, int R>
+dsa3d_status_t rows_forward_r(const Ffn& f, const FfnFwd& p, cudaStream_t st) {
+  constexpr int V = vec_width<T>();
+  const FwdWs w = fwd_ws(f, f.rows, p.ws);
+  float* y_parts = reinterpret_cast<float*>(w.h);
+  const int rows = (int)f.rows, parts = rows_parts(f, f.C, f.hidden), y_split = rows_parts(f, f.hidden, f.C);
+  RowsArgs a{};
+  a.w[0] = p.wg; a.w[1] = p.wu;
+  a.x = p.x;
+  a.out = w.sums;
+  a.K = f.C; a.N = f.hidden; a.rows = rows;
+  a.per_part = (int)ceil_div(f.C, parts);
+  dsa3d_status_t rc = launch(kKernFfnRows, st, [&] {
+    dsa3d_ffn_rows_kernel<T, R, 2, false>
+        <<<dim3((unsigned)ceil_div(f.hidden, 32 * V), (unsigned)ceil_div(f.C, a.per_part)), kRowsThreads, 0, st>>>(a);
+  });
+  if (rc != DSA3D_OK) return rc;
+  RowsArgs b{};
+  b.w[0] = p.wd;
+  b.in = w.sums;
+  b.in_parts = (int)ceil_div(f.C, a.per_part);
+  b.out = y_parts;
+  b.K = f.hidden; b.N = f.C; b.rows = rows;
+  b.per_part = (int)ceil_div(f.hidden, y_split);
+  b.act = f.act;
+  const int y_used = (int)ceil_div(f.hidden, b.per_part);
+  rc = launch(kKernFfnRows, st, [&] {
+    dsa3d_ffn_rows_kernel<T, R, 1, true><<<dim3((unsigned)ceil_div(f.C, 32 * V), (unsigned)y_used), kRowsThreads, 0, st>>>(b);
+  });
+  if (rc != DSA3D_OK) return rc;
+  const int n = rows * f.C;
+  return launch(kKernFfnReduce, st, [&] {
+    dsa3d_ffn_rows_join_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, st>>>(
+        y_parts, y_used, static_cast<const T*>(p.add), static_cast<T*>(p.y), n);
+  });
+}
+dsa3d_status_t rows_forward(const Ffn& f, const FfnFwd& p, cudaStream_t st) {
+  if (!f.f32()) return rows_forward_r<bf16, 1>(f, p, st);
+  if (f.rows == 1) return rows_forward_r<float, 1>(f, p, st);
+  if (f.rows == 2) return rows_forward_r<float, 2>(f, p, st);
+  if (f.rows <= 4) return rows_forward_r<float, 4>(f, p, st);
+  return rows_forward_r<float, 8>(f, p, st);
 }
 
 // --- tensor cores -----------------------------------------------------------------------------------
@@ -625,6 +693,7 @@ dsa3d_status_t dsa3d_gated_ffn(const void* x, const void* gate_weight, const voi
   const int64_t chunk = fit_chunk(f, workspace_bytes, fwd_bytes);
   if (chunk == 0) return DSA3D_ERR_WORKSPACE_TOO_SMALL;
   const FfnFwd p{x, gate_weight, up_weight, down_weight, add, y, workspace};
+  if (few_rows(f)) return rows_forward(f, p, stream);
   return f.f32() ? f32_forward(f, p, chunk, stream) : tc_forward(f, p, chunk, stream);
 }
 

@@ -44,6 +44,7 @@ enum KernelId {
   kKernFfnF32,
   kKernFfnReduce,
   kKernFfnPad,
+  kKernFfnRows,
   kKernFfnTcHidden,
   kKernFfnTcHiddenBwd,
   kKernFfnTcOut,
@@ -63,7 +64,7 @@ inline const char* kernel_name(int id) {
       "dsa3d_bwd_kv_tc_kernel", "dsa3d_bwd_dq_tc_kernel", "dsa3d_dwconv3d_sw_kernel",
       "dsa3d_dwconv3d_sw2_kernel", "dsa3d_layer_norm_kernel", "dsa3d_layer_norm_bwd_kernel",
       "dsa3d_norm_reduce_kernel", "dsa3d_rotary_kernel", "dsa3d_ffn_f32_kernel",
-      "dsa3d_ffn_reduce_kernel", "dsa3d_ffn_pad_kernel", "dsa3d_ffn_tc_kernel (hidden)",
+      "dsa3d_ffn_reduce_kernel", "dsa3d_ffn_pad_kernel", "dsa3d_ffn_rows_kernel", "dsa3d_ffn_tc_kernel (hidden)",
       "dsa3d_ffn_tc_kernel (hidden, backward)", "dsa3d_ffn_tc_kernel (down)", "dsa3d_ffn_tc_kernel (dx)",
       "dsa3d_ffn_tc_kernel (dw)"};
   return names[id];
