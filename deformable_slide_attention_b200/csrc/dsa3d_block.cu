@@ -208,13 +208,14 @@ dsa3d_status_t rotary_go(const void* q, const void* k, void* qo, void* ko, const
         dsa3d_rotary_kernel<T, false, HG><<<grid, kRotThreads, 0, st>>>(qt, kt, qot, kot, a);
     });
   }
-  const int64_t units = a.rows * (a.dh - a.half) * a.heads;
+  constexpr int HG_ANY = 8;
+  const int64_t units = a.rows * (a.dh - a.half) * ceil_div(a.heads, HG_ANY);
   const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(units, kRotThreads), cap);
   return launch(kKernRotary, st, [&] {
     if (interleaved)
-      dsa3d_rotary_any_kernel<T, true><<<grid, kRotThreads, 0, st>>>(qt, kt, qot, kot, a);
+      dsa3d_rotary_any_kernel<T, true, HG_ANY><<<grid, kRotThreads, 0, st>>>(qt, kt, qot, kot, a);
     else
-      dsa3d_rotary_any_kernel<T, false><<<grid, kRotThreads, 0, st>>>(qt, kt, qot, kot, a);
+      dsa3d_rotary_any_kernel<T, false, HG_ANY><<<grid, kRotThreads, 0, st>>>(qt, kt, qot, kot, a);
   });
 }
 

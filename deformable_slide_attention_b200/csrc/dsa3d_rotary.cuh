@@ -140,21 +140,38 @@ __global__ void __launch_bounds__(kRotThreads) dsa3d_rotary_kernel(const T* q, c
   }
 }
 
-// Any even dh, any alignment: one pair, or one copied dim, per unit.
-template <typename T, bool INTER>
+// Any even dh, any alignment, halves that are no whole vectors: one pair, or one copied dim, of HG heads
+// per unit (35,546 x 29 x 64 bf16 with halves of 31: 387 us with one head per unit, whose fp64 angle then
+// binds).
+template <typename T, bool INTER, int HG>
 __global__ void __launch_bounds__(kRotThreads) dsa3d_rotary_any_kernel(const T* q, const T* k, T* qo, T* ko,
                                                                       const __grid_constant__ RotArgs a) {
-  const int uph = a.half + (a.dh - 2 * a.half);
-  const int per_token = uph * a.heads;
+  const int upr = a.half + (a.dh - 2 * a.half);
+  const int groups = (a.heads + HG - 1) / HG;
+  const int per_token = upr * groups;
   const int64_t total = a.rows * per_token;
   for (int64_t unit = (int64_t)blockIdx.x * kRotThreads + threadIdx.x; unit < total;
        unit += (int64_t)gridDim.x * kRotThreads) {
     const int64_t row = unit / per_token;
     const int in = (int)(unit - row * per_token);
-    const int hd = in / uph, u = in - hd * uph;
+    const int g = in / upr, u = in - g * upr;
     const bool pair = u < a.half;
     const int d0 = pair ? (INTER ? 2 * u : u) : 2 * a.half + (u - a.half);
-    const int d1 = INTER ? d0 + 1 : d0 + a.half;
+    const int apart = pair ? (INTER ? 1 : a.half) : 0;
+    T x0[2][HG], x1[2][HG];
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      if (t == 1 && !a.has_k) break;
+      const T* src = (t ? k : q) + row * a.ld[t] + d0;
+#pragma unroll
+      for (int i = 0; i < HG; i++) {
+        const int hd = g + i * groups;
+        if (hd < a.heads) {
+          x0[t][i] = src[(int64_t)hd * a.dh];
+          x1[t][i] = src[(int64_t)hd * a.dh + apart];
+        }
+      }
+    }
     float c = 1.f, s = 0.f;
     if (pair) {
       double pos[3];
@@ -164,15 +181,19 @@ __global__ void __launch_bounds__(kRotThreads) dsa3d_rotary_any_kernel(const T* 
 #pragma unroll
     for (int t = 0; t < 2; t++) {
       if (t == 1 && !a.has_k) break;
-      const T* src = (t ? k : q) + row * a.ld[t] + (int64_t)hd * a.dh;
-      T* dst = (t ? ko : qo) + row * a.ld[2 + t] + (int64_t)hd * a.dh;
-      const T r0 = src[d0];
-      if (pair) {
-        const float x0 = to_f32(r0), x1 = to_f32(src[d1]);
-        dst[d0] = from_f32<T>(x0 * c - x1 * s);
-        dst[d1] = from_f32<T>(x0 * s + x1 * c);
-      } else {
-        dst[d0] = r0;
+      T* dst = (t ? ko : qo) + row * a.ld[2 + t] + d0;
+#pragma unroll
+      for (int i = 0; i < HG; i++) {
+        const int hd = g + i * groups;
+        if (hd >= a.heads) continue;
+        T* to = dst + (int64_t)hd * a.dh;
+        if (pair) {
+          const float y0 = to_f32(x0[t][i]), y1 = to_f32(x1[t][i]);
+          to[0] = from_f32<T>(y0 * c - y1 * s);
+          to[apart] = from_f32<T>(y0 * s + y1 * c);
+        } else {
+          to[0] = x0[t][i];
+        }
       }
     }
   }
