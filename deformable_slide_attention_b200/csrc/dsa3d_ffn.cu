@@ -64,7 +64,7 @@ int f32_parts(int64_t tiles, int64_t len) {
 }
 int f32_out_parts(const Ffn& f, int64_t rows) { return f32_parts(tiles_for(rows, f.C, kF32Tile, kF32Tile), f.hidden); }
 int f32_dw_parts(const Ffn& f, int64_t rows) {
-  return f32_parts(3 * tiles_for(f.C, f.hidden, kF32Tile, kF32Tile), rows);
+  return f32_parts(2 * tiles_for(f.C, f.hidden, kF32Tile, kF32Tile), rows);
 }
 
 // CTAs per tensor-core tile: pairs, unless the rows fill no more than one CTA's 128.
@@ -369,18 +369,26 @@ dsa3d_status_t f32_backward(const Ffn& f, const FfnBwd& p, int64_t chunk, cudaSt
     rc = f32_out(f, o, n, w.sums, parts, nullptr, at_row<float>(p.dx, r0, C), st);
     if (rc != DSA3D_OK) return rc;
     // weight gradients, summed over the chunk's tokens and added to the earlier chunks'
-    const struct { const float *a, *b; int64_t m, n; } v[3] = {{x, dg, C, H}, {x, du, C, H}, {h, dy, H, C}};
     F32Batch d{};
-    for (int i = 0; i < 3; i++) {
-      F32Args& q = d.p[i];
-      q.A[0] = {v[i].a, 1, v[i].m};
-      q.B[0] = {v[i].b, 1, v[i].n};
-      q.out[0] = w.dw_sums ? w.dw[i] : outs[i];
-      q.M = v[i].m; q.N = v[i].n; q.K = n;
-      q.products = 1; q.parts = dparts;
-      q.accumulate = r0 > 0;
+    F32Args &gu = d.p[0], &dn = d.p[1];  // dWg and dWu, then dWd
+    gu.A[0] = {x, 1, C};
+    gu.B[0] = {dg, 1, H};
+    gu.B[1] = {du, 1, H};
+    gu.M = C; gu.N = H;
+    gu.pair = true;
+    dn.A[0] = {h, 1, H};
+    dn.B[0] = {dy, 1, C};
+    dn.M = H; dn.N = C;
+    gu.out[0] = w.dw_sums ? w.dw[0] : outs[0];
+    gu.out[1] = w.dw_sums ? w.dw[1] : outs[1];
+    dn.out[0] = w.dw_sums ? w.dw[2] : outs[2];
+    for (F32Args* q : {&gu, &dn}) {
+      q->K = n;
+      q->products = 1;
+      q->parts = dparts;
+      q->accumulate = r0 > 0;
     }
-    if ((rc = f32_launch<kF32Sum>(d, 3, st)) != DSA3D_OK) return rc;
+    if ((rc = f32_launch<kF32Sum>(d, 2, st)) != DSA3D_OK) return rc;
   }
   if (!w.dw_sums) return DSA3D_OK;
   F32Join r{};

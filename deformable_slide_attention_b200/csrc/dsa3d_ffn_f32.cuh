@@ -11,7 +11,7 @@
 // one warp: 1001 x 258 x 685 took 253 us).  The next 16 are loaded into registers while these are
 // multiplied, by pointers that only move on, and two shared buffers make one barrier per step enough.
 // The products of one tile that the same outputs
-// need (gate, up and dh) are formed one after another by the same block, and the activation, its
+// need are formed by the same block (gate and up, and dWg and dWu, from one read of x; dh after them), and the activation, its
 // derivative and the element-wise products are the epilogue, so g, u and dh never reach memory.
 #pragma once
 
@@ -46,7 +46,7 @@ struct F32Operand {  // element (i, k) of an operand at p[i * si + k * sk]; si o
 };
 
 struct F32Smem {
-  float a[2][kF32K][kF32Tile + 4], b[2][kF32K][kF32Tile + 4];
+  float a[2][kF32K][kF32Tile + 4], b[2][2][kF32K][kF32Tile + 4];  // [buffer], [product][buffer]
 };
 
 // One thread's share of an operand's steps: consecutive threads along the contiguous axis, the j-th
@@ -82,41 +82,48 @@ struct F32Loader {
   }
 };
 
-// acc += A[m0.., k0..k1) . B[n0.., k0..k1); thread (ty, tx) holds rows 4 ty.., columns 4 tx..
-__device__ __forceinline__ void f32_product(float (&acc)[4][4], const F32Operand& A, const F32Operand& B, int64_t m0,
+// acc[q] += A[m0.., k0..k1) . B[q][n0.., k0..k1) for NB products that share A; thread (ty, tx) holds rows
+// 4 ty.., columns 4 tx...
+template <int NB>
+__device__ __forceinline__ void f32_product(float (*acc)[4][4], const F32Operand& A, const F32Operand* B, int64_t m0,
                                             int64_t M, int64_t n0, int64_t N, int64_t k0, int64_t k1, F32Smem& sm) {
   if (k0 >= k1) return;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  F32Loader la(A, m0, M, k0), lb(B, n0, N, k0);
+  F32Loader la(A, m0, M, k0), lb(B[0], n0, N, k0), lc(B[NB - 1], n0, N, k0);
   int left = (int)(k1 - k0), buf = 0;
-  float ra[kF32Loads], rb[kF32Loads];
-  la.fetch(ra, left);
-  lb.fetch(rb, left);
+  float ra[kF32Loads], rb[kF32Loads], rc[kF32Loads];
+  auto fetch = [&](int n) {
+    la.fetch(ra, n);
+    lb.fetch(rb, n);
+    if (NB == 2) lc.fetch(rc, n);
+  };
+  auto stash = [&](int to) {
+    la.stash(sm.a[to], ra);
+    lb.stash(sm.b[0][to], rb);
+    if (NB == 2) lc.stash(sm.b[1][to], rc);
+  };
+  fetch(left);
   __syncthreads();  // the buffers' last readers (of an earlier product) are done
-  la.stash(sm.a[0], ra);
-  lb.stash(sm.b[0], rb);
+  stash(0);
   __syncthreads();
   for (; left > 0; left -= kF32K, buf ^= 1) {
     const bool more = left > kF32K;
-    if (more) {
-      la.fetch(ra, left - kF32K);
-      lb.fetch(rb, left - kF32K);
-    }
+    if (more) fetch(left - kF32K);
 #pragma unroll
     for (int kk = 0; kk < kF32K; kk++) {
       const float4 a0 = *reinterpret_cast<const float4*>(&sm.a[buf][kk][4 * ty]);
-      const float4 b0 = *reinterpret_cast<const float4*>(&sm.b[buf][kk][4 * tx]);
       const float a[4] = {a0.x, a0.y, a0.z, a0.w};
-      const float b[4] = {b0.x, b0.y, b0.z, b0.w};
 #pragma unroll
-      for (int i = 0; i < 4; i++)
+      for (int q = 0; q < NB; q++) {
+        const float4 b0 = *reinterpret_cast<const float4*>(&sm.b[q][buf][kk][4 * tx]);
+        const float b[4] = {b0.x, b0.y, b0.z, b0.w};
 #pragma unroll
-        for (int j = 0; j < 4; j++) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) acc[q][i][j] = fmaf(a[i], b[j], acc[q][i][j]);
+      }
     }
-    if (more) {
-      la.stash(sm.a[buf ^ 1], ra);
-      lb.stash(sm.b[buf ^ 1], rb);
-    }
+    if (more) stash(buf ^ 1);
     __syncthreads();
   }
 }
@@ -124,7 +131,8 @@ __device__ __forceinline__ void f32_product(float (&acc)[4][4], const F32Operand
 enum F32Mode {
   kF32Hidden,     // out[0] = h
   kF32HiddenBwd,  // out[0] = dg, out[1] = du, out[2] = h
-  kF32Sum         // out[0] = the sum of up to two products (+ add), or this part's share of it
+  kF32Sum         // out[0] = the sum of up to two products (+ add), or this part's share of it; with `pair`
+                  // out[0] and out[1] = two products that share A[0]
 };
 
 struct F32Args {
@@ -133,7 +141,8 @@ struct F32Args {
   float* out[3];          // [M][N]; kF32Sum with parts: [part][M][N]
   int64_t M, N, K;
   int products, parts, act;
-  bool accumulate;        // kF32Sum: add to what out[0] holds
+  bool accumulate;        // kF32Sum: add to what out holds
+  bool pair;
 };
 struct F32Batch {  // blockIdx.z picks one
   F32Args p[3];
@@ -147,15 +156,18 @@ __global__ void __launch_bounds__(kF32Threads) dsa3d_ffn_f32_kernel(const __grid
   const int64_t tiles_n = (g.N + kF32Tile - 1) / kF32Tile;
   const int64_t m0 = blockIdx.x / tiles_n * kF32Tile, n0 = blockIdx.x % tiles_n * kF32Tile;
   if (m0 >= g.M) return;  // a batch's other problem has more tiles
-  constexpr int NA = MODE == kF32Hidden ? 2 : (MODE == kF32HiddenBwd ? 3 : 1);
+  constexpr int NA = MODE == kF32HiddenBwd ? 3 : 2;
   float acc[NA][4][4] = {};
   if (MODE != kF32Sum) {
-#pragma unroll
-    for (int p = 0; p < NA; p++) f32_product(acc[p], g.A[p], g.B[p], m0, g.M, n0, g.N, 0, g.K, sm);
+    f32_product<2>(acc, g.A[0], g.B, m0, g.M, n0, g.N, 0, g.K, sm);
+    if (MODE == kF32HiddenBwd) f32_product<1>(acc + NA - 1, g.A[2], g.B + 2, m0, g.M, n0, g.N, 0, g.K, sm);
   } else {
     const int64_t len = ((g.K + g.parts - 1) / g.parts + kF32K - 1) / kF32K * kF32K;
     const int64_t k0 = blockIdx.y * len, k1 = k0 + len < g.K ? k0 + len : g.K;
-    for (int p = 0; p < g.products; p++) f32_product(acc[0], g.A[p], g.B[p], m0, g.M, n0, g.N, k0, k1, sm);
+    if (g.pair)
+      f32_product<2>(acc, g.A[0], g.B, m0, g.M, n0, g.N, k0, k1, sm);
+    else
+      for (int p = 0; p < g.products; p++) f32_product<1>(acc, g.A[p], g.B + p, m0, g.M, n0, g.N, k0, k1, sm);
   }
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -167,19 +179,23 @@ __global__ void __launch_bounds__(kF32Threads) dsa3d_ffn_f32_kernel(const __grid
       if (MODE == kF32Hidden) {
         float a, da;
         f32_act(g.act, acc[0][i][j], a, da);
-        g.out[0][at] = a * acc[NA > 1 ? 1 : 0][i][j];
+        g.out[0][at] = a * acc[1][i][j];
       } else if (MODE == kF32HiddenBwd) {
         float a, da;
         f32_act(g.act, acc[0][i][j], a, da);
-        const float u = acc[NA > 1 ? 1 : 0][i][j], dh = acc[NA > 2 ? 2 : 0][i][j];
+        const float u = acc[1][i][j], dh = acc[NA - 1][i][j];
         g.out[0][at] = dh * u * da;
         g.out[1][at] = dh * a;
         g.out[2][at] = a * u;
       } else {
-        float* o = g.out[0] + (int64_t)blockIdx.y * g.M * g.N + at;
-        float v = acc[0][i][j];
-        if (g.add) v += g.add[at];
-        *o = g.accumulate ? *o + v : v;
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+          if (q == 1 && !g.pair) break;
+          float* o = g.out[q] + (int64_t)blockIdx.y * g.M * g.N + at;
+          float v = acc[q][i][j];
+          if (g.add) v += g.add[at];
+          *o = g.accumulate ? *o + v : v;
+        }
       }
     }
   }

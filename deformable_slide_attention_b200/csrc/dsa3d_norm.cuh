@@ -222,6 +222,15 @@ struct RowRing {
   __device__ __forceinline__ void wait(int64_t it) const {
     mbar_wait(bars + 8 * (uint32_t)(it % kRing), (uint32_t)(it / kRing) & 1u, abort_flag);
   }
+  // After a wait that ran out (every step is issued and waited for all the same): the copies still in
+  // flight end before the block's shared memory is released.  steps: all of the block's.
+  __device__ __forceinline__ void finish(int64_t steps) const {
+    if (threadIdx.x != 0 || *abort_flag == 0) return;
+    for (int s = 0; s < kRing; s++) {
+      const int64_t uses = steps > s ? (steps - s + kRing - 1) / kRing : 0;
+      if (uses) mbar_drain(bars + 8 * s, (uint32_t)(uses - 1) & 1u, abort_flag);
+    }
+  }
 };
 
 // This thread's vectors of R rows of tensor k of stage it % kRing; zero past the row's end or row N.
@@ -473,6 +482,7 @@ __global__ void __launch_bounds__(norm_max_threads(PER, R)) dsa3d_layer_norm_bwd
       }
     }
   }
+  if constexpr (RING) ring.finish(it);
   if (!partial) return;
   float* out = partial + (int64_t)blockIdx.x * 2 * C;
 #pragma unroll

@@ -270,6 +270,49 @@ def test_gated_ffn_large_values_stay_finite():
             assert torch.isfinite(t).all()
 
 
+# ---- sizes past 32 bits, chunks ------------------------------------------------------------------------
+def test_rows_past_32_bits_of_elements():
+    """1,100,000 x 4096 bf16 (4.5 billion elements per tensor): first, middle and last rows of the norm, its
+    dx and the rotation, against the same rows computed alone (the norm's rows do not depend on the launch)."""
+    N, C = 1100000, 4096
+    g = _gen(31)
+    x = torch.empty(N, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    w, b = _randn(g, C, mean=1.0), _randn(g, C)
+    rows = torch.tensor([0, 1, 524287, 524288, 1048575, 1048576, N - 2, N - 1], device="cuda")
+    y, _, stats = abi.layer_norm(x, w, b)
+    xs = x[rows].contiguous()
+    (ry, _, rs), (ey, es) = ref.layer_norm(xs, w, b, 1e-5, None)
+    check("y", y[rows], ry, ey)
+    check("stats", stats[:, rows], rs, es)
+    dx, _, _ = abi.layer_norm_backward(x, w, stats, y, add=x)
+    want, bound = ref.layer_norm_backward(xs, w, stats[:, rows].contiguous(), y[rows].contiguous(), xs)
+    check("dx", dx[rows], want[0], bound[0])
+    del dx
+    kw = dict(start=(0.0,) * 3, step=(1.0,) * 3, base=10000.0, interleaved=True)
+    q, _ = abi.rotary3d(x.view(N, 32, 128), None, (256, 68, 120), (44, 42, 42), out=(y.view(N, 32, 128), None), **kw)
+    for i, r in enumerate(rows.tolist()):
+        want, bound = ref.rotary(xs[i:i + 1].view(1, 32, 128), (256, 68, 120), (44, 42, 42), first=r, backward=False, **kw)
+        check("rotary", q[r:r + 1], want, bound)
+    del x, y, q
+    torch.cuda.empty_cache()
+
+
+def test_gated_ffn_of_more_tokens_than_a_chunk():
+    """66,000 tokens: a chunk of 65,536 and a short one, whole in memory for the reference."""
+    g, x, w = _ffn_inputs(66000, 32, 72, torch.bfloat16, 14)
+    dy = _randn(g, 66000, 32, dtype=torch.bfloat16)
+    check("y", abi.gated_ffn(x, *w, add=dy), *ref.gated_ffn(x, *w, "silu", dy))
+    got = abi.gated_ffn_backward(x, *w, dy)
+    want, bound = ref.gated_ffn_backward(x, *w, dy, "silu")
+    for name, o, r, e in zip(("dx", "dgate", "dup", "ddown"), got, want, bound):
+        check(name, o, r, e)
+
+
+def test_no_wait_ran_out():
+    """The bounded waits of the kernels above recorded nothing."""
+    assert abi.dsa3d_check_device(torch.cuda.current_stream().cuda_stream) == 0
+
+
 # ---- streams, graphs, sub-layers -------------------------------------------------------------------------------
 def _run_all(x, q, w, b, f, dims, axes, stream=None):
     y, h, stats = abi.layer_norm(x, w, b, add=x, stream=stream)
