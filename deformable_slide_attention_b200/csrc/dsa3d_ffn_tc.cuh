@@ -20,8 +20,8 @@
 // the results are rounded once and leave through shared memory by TMA, which also clips them to the
 // tensors' edges.  Tensor memory holds two tiles' accumulators, so that the epilogue of a tile overlaps
 // the products of the next.  kTcHiddenBwd fills it with one tile's (dh, and g and u of one half): its 16
-// warps take g and u into registers at once, so that the next half's can start, and a tile's dh follows
-// its first half's g and u, so that the columns of dh are not waited for.  (All its products are 256 columns wide: dh in tiles of 128 read shared memory for A as often
+// warps take g and u into registers at once, and a tile's dh follows its first half's g and u, so that
+// those are read while dh's products run and the columns of dh are not waited for.  (All its products are 256 columns wide: dh in tiles of 128 read shared memory for A as often
 // as for B and ran at 40% of the rate: 963 us against 690 for four 720p frames at hidden 5464.)
 //
 // The products are bound by the tensor cores (6 or 16 rows C hidden operations against a few bytes per
@@ -444,8 +444,10 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
           const int steps = (MODE == kTcDx || (MODE == kTcHiddenBwd && half == 0) ? 2 : 1) * nkb;
           for (int i = 0; ok && i < steps; i++) {
             const bool dh = MODE == kTcHiddenBwd && i >= dh_from;
-            if (MODE == kTcHiddenBwd && i == dh_from && n_tile > 0) {
-              ok = __all_sync(kFull, mbar_wait(tempty + 8, (n_tile - 1) & 1, abort_flag));
+            if (MODE == kTcHiddenBwd && i == dh_from) {
+              if (elect_one()) ft_commit<CG>(tfull);  // g and u: the epilogue reads them during dh's products
+              __syncwarp();
+              if (n_tile > 0) ok = __all_sync(kFull, mbar_wait(tempty + 8, (n_tile - 1) & 1, abort_flag));
               if (!ok) break;
             }
             ok = __all_sync(kFull, mbar_wait(full + 8 * stage, phase, abort_flag));
@@ -473,7 +475,9 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
               phase ^= 1;
             }
           }
-          if (ok && elect_one()) ft_commit<CG>(tfull + 8 * (n_acc & 1));
+          // kTcHiddenBwd: [0] g and u of a half, [1] dh of a tile; else the two buffers in turn
+          const uint32_t done = MODE == kTcHiddenBwd ? (half == 0 ? 1u : 0u) : (n_acc & 1);
+          if (ok && elect_one()) ft_commit<CG>(tfull + 8 * done);
           __syncwarp();
         }
       }
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
     const uint32_t lane_base = (uint32_t)(32 * quarter) << 16;
     const uint32_t obuf = out_base + (uint32_t)(warp - 2) * C::OUT_BUFS * kFtOutBox;
     const uint32_t free_bar = CG == 2 ? map_to_rank(tempty, 0) : tempty;
-    uint32_t n_acc = 0, n_store = 0;
+    uint32_t n_acc = 0, n_store = 0, tiles_done = 0;
     // 32 columns of this lane's row into a staging box (64-byte rows, 64-byte swizzle) and out by TMA
     auto put = [&](const void* map, const uint32_t (&v)[16], int col, int row) {
       if (lane == 0) bulk_wait_read<C::OUT_BUFS - 1>();
@@ -502,8 +506,8 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
       __syncwarp();
       if (lane == 0) ft_tma_store(map, box, col, row);
     };
-    auto acc_ready = [&]() -> bool {
-      const bool ok = __all_sync(kFull, mbar_wait(tfull + 8 * (n_acc & 1), (n_acc >> 1) & 1, abort_flag));
+    auto acc_ready = [&](uint32_t which, uint32_t parity) -> bool {
+      const bool ok = __all_sync(kFull, mbar_wait(tfull + 8 * which, parity, abort_flag));
       tc_fence_after();
       return ok;
     };
@@ -519,8 +523,9 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
       const int row0 = (int)tl.m0 + (int)rank * 128 + 32 * quarter;
       if (MODE == kTcHiddenBwd) {
         const int halves = ft_halves(g.t, tl.n0);
+        const uint32_t n_tile = tiles_done++;
         for (int half = 0; half < halves; half++, n_acc++) {
-          if (!acc_ready()) {
+          if (!acc_ready(0, n_acc & 1)) {
             alive = false;
             break;
           }
@@ -545,6 +550,10 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
             o[i] = pack_bf16(mul2(a, uu));
           }
           if (in) put(&g.o[2], o, n, row0);
+          if (half == 0 && !acc_ready(1, n_tile & 1)) {
+            alive = false;
+            break;
+          }
 #pragma unroll
           for (int c = 0; c < 2; c++) {
             uint32_t dv[16];
@@ -566,7 +575,7 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
         }
         continue;
       }
-      if (!acc_ready()) break;
+      if (!acc_ready(n_acc & 1, (n_acc >> 1) & 1)) break;
       const uint32_t buf = n_acc & 1;
       n_acc++;
       const uint32_t acc = tmem + lane_base + 256 * buf;
