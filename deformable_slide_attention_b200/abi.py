@@ -292,9 +292,15 @@ def dsa3d_timing_reset() -> None:
 
 
 # --- torch conveniences -----------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t):
@@ -611,10 +617,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _current_stream_handle():
-    """The current stream's handle without building a Stream object: small calls are bound by the host."""
-    torch = _torch()
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+def _current_stream_handle(ref):
+    """Handle of the current stream of ref's device (which _on_stream has made the current one), without
+    building a Stream object: small calls are bound by the host."""
+    return _torch()._C._cuda_getCurrentRawStream(ref.device.index)
 
 
 def _rows2d(t, name):
@@ -646,7 +652,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, add=None, out=None, want_sta
         h = None if add is None else torch.empty_like(x)
         stats = x.new_empty((2, rows), dtype=torch.float32) if want_stats else None
         _check(dsa3d_layer_norm(x.data_ptr(), _ptr(add), _ptr(weight), _ptr(bias), y.data_ptr(), _ptr(h),
-                                _ptr(stats), rows, C, eps, code, _current_stream_handle()), "dsa3d_layer_norm")
+                                _ptr(stats), rows, C, eps, code, _current_stream_handle(x)), "dsa3d_layer_norm")
     return y, (x if h is None else h), stats
 
 
@@ -674,7 +680,7 @@ def layer_norm_backward(h, weight, stats, dy, add=None, stream=None):
             ws = weight.new_empty(ws_bytes // 4)
         _check(dsa3d_layer_norm_backward(h.data_ptr(), _ptr(weight), stats.data_ptr(), dy.data_ptr(), _ptr(add),
                                          dx.data_ptr(), _ptr(dw), _ptr(db), _ptr(ws), ws_bytes, rows, C, code,
-                                         _current_stream_handle()), "dsa3d_layer_norm_backward")
+                                         _current_stream_handle(h)), "dsa3d_layer_norm_backward")
     return dx, dw, db
 
 
@@ -717,7 +723,7 @@ def _rotary(call, what, q, k, dims, axes, first, start, step, base, interleaved,
             qo = q.new_empty(q.shape)
             ko = None if k is None else k.new_empty(q.shape)
         _check(call(q.data_ptr(), _ptr(k), qo.data_ptr(), _ptr(ko), ldq, ldk, ldqo, ldko, first, rows, *dims,
-                    heads, dh, axes, start, step, base, 1 if interleaved else 0, code, _current_stream_handle()),
+                    heads, dh, axes, start, step, base, 1 if interleaved else 0, code, _current_stream_handle(q)),
                what)
     return qo, ko
 
@@ -781,7 +787,7 @@ def gated_ffn(x, gate_weight, up_weight, down_weight, activation="silu", add=Non
         ws = _ffn_workspace(workspace, dsa3d_gated_ffn_workspace_bytes(rows, C, hidden, code), x.device)
         _check(dsa3d_gated_ffn(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(), down_weight.data_ptr(),
                                _ptr(add), y.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(), rows, C, hidden,
-                               _ACTIVATIONS[activation], code, _current_stream_handle()), "dsa3d_gated_ffn")
+                               _ACTIVATIONS[activation], code, _current_stream_handle(x)), "dsa3d_gated_ffn")
     return y
 
 
@@ -802,6 +808,6 @@ def gated_ffn_backward(x, gate_weight, up_weight, down_weight, dy, activation="s
         _check(dsa3d_gated_ffn_backward(x.data_ptr(), gate_weight.data_ptr(), up_weight.data_ptr(),
                                         down_weight.data_ptr(), dy.data_ptr(), *(t.data_ptr() for t in grads),
                                         _ptr(ws), 0 if ws is None else ws.numel(), rows, C, hidden,
-                                        _ACTIVATIONS[activation], code, _current_stream_handle()),
+                                        _ACTIVATIONS[activation], code, _current_stream_handle(x)),
                "dsa3d_gated_ffn_backward")
     return grads

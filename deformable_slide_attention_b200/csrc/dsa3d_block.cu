@@ -55,7 +55,8 @@ NormPlan norm_plan(int C, dsa3d_dtype_t dtype, int odd_per) {
 }
 // Blocks: enough to fill the GPU, each then strides over the rest of the rows.
 int norm_blocks(const NormPlan& p, int64_t rows, int per_sm) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(rows, (int64_t)p.ty * p.r), (int64_t)sm_count() * per_sm));
+  const int64_t steps = ceil_div(rows, (int64_t)p.ty * p.r);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(steps, (int64_t)sm_count() * per_sm));
 }
 NormPlan norm_fwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype) {
   NormPlan p = norm_plan(C, dtype, 8);

@@ -429,7 +429,8 @@ dsa3d_status_t rows_forward_r(const Ffn& f, const FfnFwd& p, cudaStream_t st) {
   b.act = f.act;
   const int y_used = (int)ceil_div(f.hidden, b.per_part);
   rc = launch(kKernFfnRows, st, [&] {
-    dsa3d_ffn_rows_kernel<T, R, 1, true><<<dim3((unsigned)ceil_div(f.C, 32 * V), (unsigned)y_used), kRowsThreads, 0, st>>>(b);
+    dsa3d_ffn_rows_kernel<T, R, 1, true>
+        <<<dim3((unsigned)ceil_div(f.C, 32 * V), (unsigned)y_used), kRowsThreads, 0, st>>>(b);
   });
   if (rc != DSA3D_OK) return rc;
   const int n = rows * f.C;

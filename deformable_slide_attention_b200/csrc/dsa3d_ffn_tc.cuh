@@ -1,7 +1,7 @@
 // dsa3d_ffn_tc.cuh -- the gated feed-forward block's products on the tensor cores (bf16, sm_100a):
 //
 //   kTcHidden     h = act(x Wg) * (x Wu)                                one tile: 128 columns of g and of u
-//   kTcHiddenBwd  dh = dy Wd^T for 256 columns, then g and u for two halves of 128: dg = dh u act'(g),
+//   kTcHiddenBwd  dh = dy Wd^T for 256 columns, g and u for each of their halves: dg = dh u act'(g),
 //                 du = dh act(g), h = act(g) u
 //   kTcOut        y = h Wd (+ add), whole or in parts of the summed axis
 //   kTcDx         dx = dg Wg^T + du Wu^T                                one accumulator over both products
@@ -21,11 +21,15 @@
 // tensors' edges.  Tensor memory holds two tiles' accumulators, so that the epilogue of a tile overlaps
 // the products of the next.  kTcHiddenBwd fills it with one tile's (dh, and g and u of one half): its 16
 // warps take g and u into registers at once, and a tile's dh follows its first half's g and u, so that
-// those are read while dh's products run and the columns of dh are not waited for.  (All its products are 256 columns wide: dh in tiles of 128 read shared memory for A as often
-// as for B and ran at 40% of the rate: 963 us against 690 for four 720p frames at hidden 5464.)
+// those are read while dh's products run and the columns of dh are not waited for.  (All its products are
+// 256 columns wide: dh in tiles of 128 read shared memory for A as often as for B, and a step took 658
+// cycles instead of 256, whatever the number of stages.)
 //
 // The products are bound by the tensor cores (6 or 16 rows C hidden operations against a few bytes per
-// element).  Waits are bounded (dsa3d_tc.cuh); no load is multicast.
+// element).  Four 720p frames (14,400 x 2048), hidden 5464, TFLOP/s over a long run under the power cap:
+// hidden values 1300, y 1260, their backward 980, dx 1280, weight gradients 1290; a library product of
+// these sizes 1150 to 1200 and 1430 at 8192^3.  The tensor pipe is busy 80 to 88% of the cycles, 62% in
+// kTcHiddenBwd.  Waits are bounded (dsa3d_tc.cuh); no load is multicast.
 #pragma once
 
 #include <cuda.h>
@@ -49,8 +53,8 @@ template <int MODE, int CG>
 struct FtCfg {
   static constexpr bool kGated = MODE == kTcHidden || MODE == kTcHiddenBwd;
   static constexpr int TILE_M = 128 * CG;
-  static constexpr int TILE_N = MODE == kTcHidden ? 128 : 256;  // output columns per tile
-  static constexpr int HALVES = MODE == kTcHiddenBwd ? 2 : 1;   // of a tile, each with its own epilogue
+  // output columns per tile; kTcHiddenBwd's epilogue takes them in halves of 128
+  static constexpr int TILE_N = MODE == kTcHidden ? 128 : 256;
   static constexpr int EPI_WARPS = MODE == kTcHiddenBwd ? 16 : 8;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
   static constexpr int PRODUCTS = MODE == kTcHiddenBwd ? 3 : (MODE == kTcDx ? 2 : 1);  // steps per k-block
@@ -461,11 +465,13 @@ __global__ void __launch_bounds__(FtCfg<MODE, CG>::THREADS, 1) dsa3d_ffn_tc_kern
               if (MODE == kTcHiddenBwd && dh) {
 #pragma unroll
                 for (int k = 0; k < kFtK / 16; k++)
-                  ft_mma<CG>(d, da + (uint64_t)(k * A_STEP >> 4), db + (uint64_t)(k * 32 >> 4), ID_DH, k > 0 ? 1u : more);
+                  ft_mma<CG>(d, da + (uint64_t)(k * A_STEP >> 4), db + (uint64_t)(k * 32 >> 4), ID_DH,
+                           k > 0 ? 1u : more);
               } else {
 #pragma unroll
                 for (int k = 0; k < kFtK / 16; k++)
-                  ft_mma<CG>(d, da + (uint64_t)(k * A_STEP >> 4), db + (uint64_t)(k * B_STEP >> 4), ID, k > 0 ? 1u : more);
+                  ft_mma<CG>(d, da + (uint64_t)(k * A_STEP >> 4), db + (uint64_t)(k * B_STEP >> 4), ID,
+                           k > 0 ? 1u : more);
               }
               ft_commit<CG>(empty + 8 * stage);
             }

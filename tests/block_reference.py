@@ -90,13 +90,14 @@ def act(g, name):
 
 def _hidden(x, wg, wu, name, u):
     """h and the parts a backward needs, with the error of g and u (C products summed in fp32; the
-    activations and their derivatives change by at most 1.13 and 1 per unit of g, and __expf and erff
-    add a few units)."""
+    activations and their derivatives change by at most 1.13 and 1 per unit of g)."""
     C = x.shape[1]
     g, up = x @ wg, x @ wu
     eg, eu = (C + 8) * F32 * (x.abs() @ wg.abs()), (C + 8) * F32 * (x.abs() @ wu.abs())
     a, da = act(g, name)
-    e_fn = (2.0 ** -17 if u > 1e-5 else 2.0 ** -20)  # relative error of exp at |g| up to about 20
+    # relative error of the exponentials at |g| up to about 20 (bf16: approximate ones, of 2^-22 of their
+    # argument's magnitude), reciprocals and erfc
+    e_fn = 2.0 ** -17 if u > 1e-5 else 2.0 ** -20
     ea, eda = 1.13 * eg + e_fn * (a.abs() + 1e-3), eg + e_fn * (da.abs() + 1e-3)
     h = a * up
     eh = ea * up.abs() + a.abs() * eu + u * h.abs()

@@ -147,7 +147,7 @@ def calls(monkeypatch):
         monkeypatch.setattr(abi, name, lambda *a, _n=name: log.append((_n, a)) or 0)
     monkeypatch.setattr(abi, "_on_device", lambda *a: None)
     monkeypatch.setattr(abi, "_on_stream", lambda *a: contextlib.nullcontext())
-    monkeypatch.setattr(abi, "_current_stream_handle", lambda: 0)
+    monkeypatch.setattr(abi, "_current_stream_handle", lambda ref: 0)
     return log
 
 

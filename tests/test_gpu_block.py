@@ -205,8 +205,9 @@ def test_rotary3d_keeps_scores_and_undoes_itself():
 
 # ---- gated feed-forward -------------------------------------------------------------------------------------
 FFN_SHAPES = [(1, 1, 1), (3, 5, 7), (1, 64, 160), (7, 64, 160), (65, 40, 72), (130, 258, 685), (200, 512, 1024),
-              (129, 128, 264), (1000, 72, 200), (16, 2048, 1032), (300, 1000, 520), (1, 2048, 1001), (700, 131, 257), (150, 64, 259), (2, 64, 160), (3, 520, 1032),
-              (4, 2048, 40), (4, 8, 4104), (5, 2048, 1032), (8, 520, 264), (9, 264, 520), (257, 64, 2048), (0, 64, 96)]
+              (129, 128, 264), (1000, 72, 200), (16, 2048, 1032), (300, 1000, 520), (1, 2048, 1001), (700, 131, 257),
+              (150, 64, 259), (2, 64, 160), (3, 520, 1032), (4, 2048, 40), (4, 8, 4104), (5, 2048, 1032), (8, 520, 264),
+              (9, 264, 520), (257, 64, 2048), (0, 64, 96)]
 
 
 def _ffn_inputs(rows, C, hidden, dtype, seed, std=1.0):
