@@ -62,9 +62,9 @@ int f32_parts(int64_t tiles, int64_t len) {
   const int64_t p = std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 8, (int64_t)kFfnMaxParts}));
   return (int)ceil_div(steps, ceil_div(steps, p));
 }
-int f32_out_parts(const Ffn& f, int64_t rows) { return f32_parts(tiles_for(rows, f.C, kF32Tile, kF32Tile), f.hidden); }
+int f32_out_parts(const Ffn& f, int64_t rows) { return f32_parts(tiles_for(rows, f.C, 64, kF32Cols), f.hidden); }
 int f32_dw_parts(const Ffn& f, int64_t rows) {
-  return f32_parts(2 * tiles_for(f.C, f.hidden, kF32Tile, kF32Tile), rows);
+  return f32_parts(2 * tiles_for(f.C, f.hidden, 64, kF32Cols), rows);
 }
 
 // CTAs per tensor-core tile: pairs, unless the rows fill no more than one CTA's 128.
@@ -273,14 +273,22 @@ struct FfnBwd {
 };
 
 // --- fp32 -------------------------------------------------------------------------------------------
-template <int MODE>
-dsa3d_status_t f32_launch(const F32Batch& b, int problems, cudaStream_t st) {
+template <int MODE, int TM>
+dsa3d_status_t f32_launch_rows(const F32Batch& b, int problems, cudaStream_t st) {
   int64_t tiles = 0;
-  for (int i = 0; i < problems; i++) tiles = std::max(tiles, tiles_for(b.p[i].M, b.p[i].N, kF32Tile, kF32Tile));
+  for (int i = 0; i < problems; i++) tiles = std::max(tiles, tiles_for(b.p[i].M, b.p[i].N, TM, kF32Cols));
   if (tiles > INT_MAX) return DSA3D_ERR_UNSUPPORTED;
   return launch(kKernFfnF32, st, [&] {
-    dsa3d_ffn_f32_kernel<MODE><<<dim3((unsigned)tiles, b.p[0].parts, problems), kF32Threads, 0, st>>>(b);
+    dsa3d_ffn_f32_kernel<MODE, TM><<<dim3((unsigned)tiles, b.p[0].parts, problems), f32_threads(TM), 0, st>>>(b);
   });
+}
+// Tiles of 64 rows, or of 32 where those make fewer than four blocks per SM: finer blocks even out the SMs.
+template <int MODE>
+dsa3d_status_t f32_launch(const F32Batch& b, int problems, cudaStream_t st) {
+  int64_t blocks = 0;
+  for (int i = 0; i < problems; i++) blocks += tiles_for(b.p[i].M, b.p[i].N, 64, kF32Cols) * b.p[0].parts;
+  return blocks < 4 * (int64_t)sm_count() ? f32_launch_rows<MODE, 32>(b, problems, st)
+                                          : f32_launch_rows<MODE, 64>(b, problems, st);
 }
 
 dsa3d_status_t f32_join(const F32Join& r, int outputs, cudaStream_t st) {

@@ -7,9 +7,9 @@
 // fp32 products stay fp32 here: the tensor cores' tf32 keeps 11 bits of each factor, and sums of split
 // bf16 factors are cut, not rounded, at every step of the accumulator.  The kernel is bound by the fp32
 // FMA pipes, or, at a few hundred tokens, by how many of them the tiles reach (backward of 1001 x 258 x
-// 685: 178 us, 16 TFLOP/s).  Tiles of 64 x 64 outputs, 16 along the summed axis, 256 threads with 4 x 4
-// sums each (128 threads with 8 x 4 leave a scheduler one warp: 253 us).  The next 16 are loaded into
-// registers while these are
+// 685: 178 us with tiles of 64 rows everywhere).  Tiles of 64 x 64 outputs (32 x 64 where those would
+// leave SMs idle), 16 along the summed axis, 4 x 4 sums per thread (8 x 4 leave a scheduler one warp: 253
+// us).  The next 16 are loaded into registers while these are
 // multiplied, by pointers that only move on, and two shared buffers make one barrier per step enough.
 // The products of one tile that the same outputs
 // need are formed by the same block (gate and up, and dWg and dWu, from one read of x; dh after them), and the activation, its
@@ -38,61 +38,66 @@ __device__ __forceinline__ void f32_act(int act, float g, float& a, float& da) {
   }
 }
 
-constexpr int kF32Tile = 64, kF32K = 16, kF32Threads = 256;
-constexpr int kF32Loads = kF32Tile * kF32K / kF32Threads;  // elements of each operand per thread and step
+constexpr int kF32Cols = 64, kF32K = 16;
+constexpr int f32_threads(int TM) { return TM * kF32Cols / 16; }  // 4 x 4 sums each
 
 struct F32Operand {  // element (i, k) of an operand at p[i * si + k * sk]; si or sk is 1
   const float* p;
   int64_t si, sk;
 };
 
+template <int TM>
 struct F32Smem {
-  float a[2][kF32K][kF32Tile + 4], b[2][2][kF32K][kF32Tile + 4];  // [buffer], [product][buffer]
+  float a[2][kF32K][TM + 4], b[2][2][kF32K][kF32Cols + 4];  // [buffer], [product][buffer]
 };
 
-// One thread's share of an operand's steps: consecutive threads along the contiguous axis, the j-th
-// element `apart` behind the first; the pointer moves on by 16 of the summed axis per step.
+// One thread's share of an operand's steps (ROWS x 16 of them over T threads): consecutive threads along
+// the contiguous axis, the j-th element `apart` behind the first; the pointer moves on by 16 of the
+// summed axis per step.
+template <int ROWS, int T>
 struct F32Loader {
+  static constexpr int kLoads = ROWS * kF32K / T;
   const float* p;
   int64_t apart, step;
   int i, k, di, dk;    // position in the tile, and from element to element
   unsigned inside;     // bit j: element j's row lies inside the operand
   __device__ __forceinline__ F32Loader(const F32Operand& o, int64_t i0, int64_t ni, int64_t k0) {
     const bool along_k = o.sk == 1;
-    i = along_k ? threadIdx.x / kF32K : threadIdx.x % kF32Tile;
-    k = along_k ? threadIdx.x % kF32K : threadIdx.x / kF32Tile;
-    di = along_k ? kF32Threads / kF32K : 0;
-    dk = along_k ? 0 : kF32Threads / kF32Tile;
+    i = along_k ? threadIdx.x / kF32K : threadIdx.x % ROWS;
+    k = along_k ? threadIdx.x % kF32K : threadIdx.x / ROWS;
+    di = along_k ? T / kF32K : 0;
+    dk = along_k ? 0 : T / ROWS;
     apart = di * o.si + dk * o.sk;
     step = kF32K * o.sk;
     p = o.p + (i0 + i) * o.si + (k0 + k) * o.sk;
     inside = 0;
 #pragma unroll
-    for (int j = 0; j < kF32Loads; j++) inside |= (i0 + i + j * di < ni ? 1u : 0u) << j;
+    for (int j = 0; j < kLoads; j++) inside |= (i0 + i + j * di < ni ? 1u : 0u) << j;
   }
   // left: elements of the summed axis from this step on
-  __device__ __forceinline__ void fetch(float (&r)[kF32Loads], int left) {
+  __device__ __forceinline__ void fetch(float (&r)[kLoads], int left) {
 #pragma unroll
-    for (int j = 0; j < kF32Loads; j++)
+    for (int j = 0; j < kLoads; j++)
       r[j] = ((inside >> j) & 1u) && k + j * dk < left ? __ldg(p + j * apart) : 0.f;
     p += step;
   }
-  __device__ __forceinline__ void stash(float (&dst)[kF32K][kF32Tile + 4], const float (&r)[kF32Loads]) const {
+  __device__ __forceinline__ void stash(float (&dst)[kF32K][ROWS + 4], const float (&r)[kLoads]) const {
 #pragma unroll
-    for (int j = 0; j < kF32Loads; j++) dst[k + j * dk][i + j * di] = r[j];
+    for (int j = 0; j < kLoads; j++) dst[k + j * dk][i + j * di] = r[j];
   }
 };
 
 // acc[q] += A[m0.., k0..k1) . B[q][n0.., k0..k1) for NB products that share A; thread (ty, tx) holds rows
 // 4 ty.., columns 4 tx...
-template <int NB>
+template <int NB, int TM>
 __device__ __forceinline__ void f32_product(float (*acc)[4][4], const F32Operand& A, const F32Operand* B, int64_t m0,
-                                            int64_t M, int64_t n0, int64_t N, int64_t k0, int64_t k1, F32Smem& sm) {
+                                            int64_t M, int64_t n0, int64_t N, int64_t k0, int64_t k1, F32Smem<TM>& sm) {
   if (k0 >= k1) return;
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  F32Loader la(A, m0, M, k0), lb(B[0], n0, N, k0), lc(B[NB - 1], n0, N, k0);
+  F32Loader<TM, f32_threads(TM)> la(A, m0, M, k0);
+  F32Loader<kF32Cols, f32_threads(TM)> lb(B[0], n0, N, k0), lc(B[NB - 1], n0, N, k0);
   int left = (int)(k1 - k0), buf = 0;
-  float ra[kF32Loads], rb[kF32Loads], rc[kF32Loads];
+  float ra[decltype(la)::kLoads], rb[decltype(lb)::kLoads], rc[decltype(lc)::kLoads];
   auto fetch = [&](int n) {
     la.fetch(ra, n);
     lb.fetch(rb, n);
@@ -149,13 +154,13 @@ struct F32Batch {  // blockIdx.z picks one
   F32Args p[3];
 };
 
-template <int MODE>
-__global__ void __launch_bounds__(kF32Threads) dsa3d_ffn_f32_kernel(const __grid_constant__ F32Batch batch) {
-  __shared__ __align__(16) F32Smem sm;
+template <int MODE, int TM>
+__global__ void __launch_bounds__(f32_threads(TM)) dsa3d_ffn_f32_kernel(const __grid_constant__ F32Batch batch) {
+  __shared__ __align__(16) F32Smem<TM> sm;
   const F32Args& g = batch.p[MODE == kF32Sum ? blockIdx.z : 0];
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  const int64_t tiles_n = (g.N + kF32Tile - 1) / kF32Tile;
-  const int64_t m0 = blockIdx.x / tiles_n * kF32Tile, n0 = blockIdx.x % tiles_n * kF32Tile;
+  const int64_t tiles_n = (g.N + kF32Cols - 1) / kF32Cols;
+  const int64_t m0 = blockIdx.x / tiles_n * TM, n0 = blockIdx.x % tiles_n * kF32Cols;
   if (m0 >= g.M) return;  // a batch's other problem has more tiles
   constexpr int NA = MODE == kF32HiddenBwd ? 3 : 2;
   float acc[NA][4][4] = {};

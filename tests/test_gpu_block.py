@@ -342,6 +342,52 @@ def test_on_another_stream_and_from_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(r, want))
 
 
+def test_beside_the_attention_on_another_stream():
+    """The feed-forward block and the attention, both with tensor memory of their own, on two streams at
+    once, several times over: each as when it runs alone."""
+    from deformable_slide_attention_b200 import inputs
+    dims, heads, dh, window = (16, 32, 32), 4, 64, (3, 7, 7)
+    _, inp = inputs.custom(*dims, heads, dh, window, "bf16", seed=9, scale=2.0)
+    d = {k: v.cuda() for k, v in inp.items()}
+    g, x, w = _ffn_inputs(6000, 512, 1032, torch.bfloat16, 3)
+    dy = _randn(g, 6000, 512, dtype=torch.bfloat16)
+
+    def attention():
+        out, lse = abi.forward(d["q"], d["k"], d["v"], d["offsets"], dims, window)
+        return (out, *abi.backward(d["q"], d["k"], d["v"], d["offsets"], lse, d["dout"], dims, window)[:3])
+
+    def block():
+        return (abi.gated_ffn(x, *w), *abi.gated_ffn_backward(x, *w, dy))
+    want = attention(), block()
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(5):
+        for s, f, ref_ in zip(streams, (attention, block), want):
+            with torch.cuda.stream(s):
+                got.append((f(), ref_))
+    torch.cuda.synchronize()
+    for r, ref_ in got:
+        assert all(torch.equal(a, b) for a, b in zip(r, ref_))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,C,hidden", [(300, 72, 136), (70, 61, 77), (6, 64, 96)])
+def test_gated_ffn_rows_do_not_touch_each_other(dtype, rows, C, hidden):
+    """A token with a NaN or an infinity: its own y and dx are not finite, every other row's are what they
+    are without it."""
+    g, x, w = _ffn_inputs(rows, C, hidden, DT[dtype], 2)
+    dy = _randn(g, rows, C, dtype=DT[dtype])
+    y0, dx0 = abi.gated_ffn(x, *w), abi.gated_ffn_backward(x, *w, dy)[0]
+    x[1, 2], x[rows - 2, C - 1] = float("nan"), float("inf")
+    y, dx = abi.gated_ffn(x, *w), abi.gated_ffn_backward(x, *w, dy)[0]
+    keep = [r for r in range(rows) if r not in (1, rows - 2)]
+    assert torch.equal(y[keep], y0[keep]) and torch.equal(dx[keep], dx0[keep])
+    assert not torch.isfinite(y[1]).any() and not torch.isfinite(y[rows - 2]).any()
+
+
 def test_captured_and_replayed_with_new_inputs():
     args = _all_inputs()
     _run_all(*args)
