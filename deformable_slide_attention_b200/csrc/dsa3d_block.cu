@@ -378,10 +378,8 @@ dsa3d_status_t dsa3d_layer_norm_backward(const void* h, const float* weight, con
     st = p.v == 8 ? norm_bwd<__nv_bfloat16, 8>(a, p, stream)
                   : norm_bwd<__nv_bfloat16, 1>(a, p, stream);
   if (st != DSA3D_OK || !weight) return st;
-  return launch(kKernNormReduce, stream, [&] {
-    dsa3d_norm_reduce_kernel<<<(unsigned)ceil_div(2 * (int64_t)C, 32), dim3(32, 32), 0, stream>>>(
-        partial, p.blocks, C, dweight, dbias);
-  });
+  return launch_early(kKernNormReduce, stream, dsa3d_norm_reduce_kernel, dim3((unsigned)ceil_div(2 * (int64_t)C, 32)),
+                      dim3(32, 32), partial, p.blocks, C, dweight, dbias);
 }
 
 dsa3d_status_t dsa3d_rotary3d(const void* q, const void* k, void* q_out, void* k_out, long long ldq,

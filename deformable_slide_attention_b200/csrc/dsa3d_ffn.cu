@@ -148,8 +148,8 @@ struct Carver {
 };
 
 // A forward of so few tokens that the weights' bytes bind, with rows of whole 16-byte vectors.  C 4096,
-// hidden 10,944: bf16, one token 62 us against 70 through the tensor-core tiles, two 99 against 70; fp32,
-// four tokens 137 us against 987 through the tiles of 64.
+// hidden 10,944: bf16, one token 57 us against 70 through the tensor-core tiles, two 99 against 70; fp32,
+// four tokens 137 us against 987 through the tiles of 64 rows.
 bool few_rows(const Ffn& f) {
   const int v = f.f32() ? 4 : 8;
   return f.rows <= (f.f32() ? kRowsMaxF32 : kRowsMaxBf16) && f.C % v == 0 && f.hidden % v == 0;
@@ -295,7 +295,7 @@ dsa3d_status_t f32_join(const F32Join& r, int outputs, cudaStream_t st) {
   int64_t most = 0;
   for (int i = 0; i < outputs; i++) most = std::max(most, r.n[i]);
   const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(most, 256), (int64_t)sm_count() * 8);
-  return launch(kKernFfnReduce, st, [&] { dsa3d_ffn_join_kernel<<<dim3(grid, outputs), 256, 0, st>>>(r); });
+  return launch_early(kKernFfnReduce, st, dsa3d_ffn_join_kernel, dim3(grid, outputs), dim3(256), r);
 }
 
 // y or dx from up to two products over hidden, in parts where the plan has them.
@@ -436,16 +436,12 @@ dsa3d_status_t rows_forward_r(const Ffn& f, const FfnFwd& p, cudaStream_t st) {
   b.per_part = (int)ceil_div(f.hidden, y_split);
   b.act = f.act;
   const int y_used = (int)ceil_div(f.hidden, b.per_part);
-  rc = launch(kKernFfnRows, st, [&] {
-    dsa3d_ffn_rows_kernel<T, R, 1, true>
-        <<<dim3((unsigned)ceil_div(f.C, 32 * V), (unsigned)y_used), kRowsThreads, 0, st>>>(b);
-  });
+  rc = launch_early(kKernFfnRows, st, dsa3d_ffn_rows_kernel<T, R, 1, true>,
+                    dim3((unsigned)ceil_div(f.C, 32 * V), (unsigned)y_used), dim3(kRowsThreads), b);
   if (rc != DSA3D_OK) return rc;
   const int n = rows * f.C;
-  return launch(kKernFfnReduce, st, [&] {
-    dsa3d_ffn_rows_join_kernel<T><<<(unsigned)ceil_div(n, 256), 256, 0, st>>>(
-        y_parts, y_used, static_cast<const T*>(p.add), static_cast<T*>(p.y), n);
-  });
+  return launch_early(kKernFfnReduce, st, dsa3d_ffn_rows_join_kernel<T>, dim3((unsigned)ceil_div(n, 256)), dim3(256),
+                      y_parts, y_used, static_cast<const T*>(p.add), static_cast<T*>(p.y), n);
 }
 dsa3d_status_t rows_forward(const Ffn& f, const FfnFwd& p, cudaStream_t st) {
   if (!f.f32()) return rows_forward_r<bf16, 1>(f, p, st);
@@ -566,7 +562,7 @@ dsa3d_status_t tc_join(const FtTiles& t, int cg, const bf16* add, void* o0, void
   // about eight blocks per SM over the tail's tiles, of four rows or more
   const int64_t tail = tiles - t.full;
   const unsigned by = (unsigned)std::max<int64_t>(1, std::min(ceil_div(rows, 4), (int64_t)sm_count() * 8 / tail));
-  return launch(kKernFfnReduce, st, [&] { dsa3d_ffn_tail_kernel<<<dim3((unsigned)tail, by), 256, 0, st>>>(a); });
+  return launch_early(kKernFfnReduce, st, dsa3d_ffn_tail_kernel, dim3((unsigned)tail, by), dim3(256), a);
 }
 
 // y or dx: one launch, and the joining of its tail where it has one.

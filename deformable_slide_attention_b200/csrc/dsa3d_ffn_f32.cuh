@@ -7,7 +7,7 @@
 // fp32 products stay fp32 here: the tensor cores' tf32 keeps 11 bits of each factor, and sums of split
 // bf16 factors are cut, not rounded, at every step of the accumulator.  The kernel is bound by the fp32
 // FMA pipes, or, at a few hundred tokens, by how many of them the tiles reach (backward of 1001 x 258 x
-// 685: 178 us with tiles of 64 rows everywhere).  Tiles of 64 x 64 outputs (32 x 64 where those would
+// 685: 160 us, 18 TFLOP/s; 178 with tiles of 64 rows everywhere).  Tiles of 64 x 64 outputs (32 x 64 where those would
 // leave SMs idle), 16 along the summed axis, 4 x 4 sums per thread (8 x 4 leave a scheduler one warp: 253
 // us).  The next 16 are loaded into registers while these are
 // multiplied, by pointers that only move on, and two shared buffers make one barrier per step enough.
@@ -217,6 +217,7 @@ struct F32Join {
   int parts;
 };
 __global__ void __launch_bounds__(256) dsa3d_ffn_join_kernel(const __grid_constant__ F32Join r) {
+  prior_kernel_done();
   const int p = blockIdx.y;
   const int64_t n = r.n[p], step = (int64_t)gridDim.x * blockDim.x;
   const float* __restrict__ from = r.partial[p];

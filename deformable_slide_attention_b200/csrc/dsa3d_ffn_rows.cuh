@@ -6,8 +6,8 @@
 // through the workspace (the strips alone would leave most SMs idle).  Rows of g and u are joined,
 // activated and multiplied by the blocks of the second product that need them, whose first weights are
 // loading meanwhile, and y's parts are joined by a last small launch.
-// One bf16 token at C 4096, hidden 10,944: 269 MB of weights in 62 us (4.4 TB/s over the three launches;
-// three or more blocks per SM: 70 us and more).
+// One bf16 token at C 4096, hidden 10,944: 269 MB of weights in 57 us (4.7 TB/s over the three launches, of
+// which the later two start early; 63 us without that, three or more blocks per SM 70 us and more).
 
 #pragma once
 
@@ -59,7 +59,10 @@ __global__ void __launch_bounds__(kRowsThreads) dsa3d_ffn_rows_kernel(const __gr
     }
   };
   Vec<T, V> cur[UNROLL][NW];
-  load(cur, warp);  // on its way while the row operand is formed
+  load(cur, warp);  // on its way while the row operand is formed (and, of the second product, while the
+                    // first launch ends: the weights do not depend on it)
+  next_kernel_may_start();
+  if (GATED) prior_kernel_done();
   for (int i = threadIdx.x; i < len; i += kRowsThreads) {
 #pragma unroll
     for (int r = 0; r < R; r++) {
@@ -132,6 +135,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) dsa3d_ffn_rows_join_kernel(const float* __restrict__ partial, int parts,
                                                                   const T* add, T* y, int n) {
   const int i = blockIdx.x * 256 + threadIdx.x;
+  prior_kernel_done();
   if (i >= n) return;
   float v = 0.f;
 #pragma unroll 8

@@ -677,6 +677,7 @@ __global__ void __launch_bounds__(256) dsa3d_ffn_tail_kernel(const __grid_consta
   int problem;
   int64_t m0, n0;
   ft_place(a.t, a.t.full + blockIdx.x, a.tile_m, 256, problem, m0, n0);
+  prior_kernel_done();
   const int64_t M = a.t.M[problem], N = a.t.N[problem];
   const int c = 4 * (threadIdx.x & 63);
   const int64_t n = n0 + c;

@@ -53,5 +53,21 @@ dsa3d_status_t launch(int kernel_id, cudaStream_t st, F&& f) {
   return (tl.finish() && launched) ? DSA3D_OK : DSA3D_ERR_CUDA;
 }
 
+// A launch whose blocks may start while the stream's previous kernel is still running; the kernel calls
+// prior_kernel_done() before it touches what that kernel writes.
+template <typename... P, typename... A>
+dsa3d_status_t launch_early(int kernel_id, cudaStream_t st, void (*kern)(P...), dim3 grid, dim3 block, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return launch(kernel_id, st, [&] { cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...); });
+}
+
 }  // namespace host
 }  // namespace dsa3d

@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(norm_max_threads(PER, R)) dsa3d_layer_norm_bwd
     }
   }
   if constexpr (RING) ring.finish(it);
+  next_kernel_may_start();
   if (!partial) return;
   float* out = partial + (int64_t)blockIdx.x * 2 * C;
 #pragma unroll
@@ -518,6 +519,7 @@ __global__ void __launch_bounds__(1024) dsa3d_norm_reduce_kernel(const float* __
   const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
   const int64_t width = 2 * (int64_t)C;
   float v = 0.f;
+  prior_kernel_done();
   if (col < width) {
 #pragma unroll 4
     for (int p = threadIdx.y; p < P; p += 32) v += partial[p * width + col];

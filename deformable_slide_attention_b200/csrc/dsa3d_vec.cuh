@@ -17,6 +17,11 @@ __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// For kernels launched early (launch_early): waits until the stream's previous kernel is complete and its
+// writes are visible; and, in that previous kernel, allows the next one's blocks to start.
+__device__ __forceinline__ void prior_kernel_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Two fp32 values in 64 bits: one instruction for two sums, products or multiply-adds.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
