@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
+import operator
 import os
 import threading
 
@@ -117,6 +119,17 @@ def _load():
 
 
 _INT3, _DBL3 = ctypes.c_int * 3, ctypes.c_double * 3
+
+
+@functools.lru_cache(maxsize=256)
+def _three(kind, values):
+    """A C array of three numbers; the library only reads it."""
+    return kind(*values)
+
+
+def _axes(axes, start, step):
+    return (_three(_INT3, tuple(map(operator.index, axes))), _three(_DBL3, tuple(map(float, start))),
+            _three(_DBL3, tuple(map(float, step))))
 
 
 class KernelTime(ctypes.Structure):
@@ -238,15 +251,14 @@ def dsa3d_rotary3d(q, k, q_out, k_out, ldq, ldk, ldqo, ldko, first, rows, F, Hp,
                    start, step, base, interleaved, dtype, stream) -> int:
     """Rotary positions of the token grid for q and k; axes, start and step are sequences of three."""
     return _load().dsa3d_rotary3d(q, k, q_out, k_out, ldq, ldk, ldqo, ldko, first, rows, F, Hp, Wp, heads,
-                                  dh, _INT3(*axes), _DBL3(*start), _DBL3(*step), base, interleaved, dtype,
-                                  stream)
+                                  dh, *_axes(axes, start, step), base, interleaved, dtype, stream)
 
 
 def dsa3d_rotary3d_backward(dq_out, dk_out, dq, dk, lddqo, lddko, lddq, lddk, first, rows, F, Hp, Wp, heads,
                             dh, axes, start, step, base, interleaved, dtype, stream) -> int:
     return _load().dsa3d_rotary3d_backward(dq_out, dk_out, dq, dk, lddqo, lddko, lddq, lddk, first, rows, F,
-                                           Hp, Wp, heads, dh, _INT3(*axes), _DBL3(*start), _DBL3(*step), base,
-                                           interleaved, dtype, stream)
+                                           Hp, Wp, heads, dh, *_axes(axes, start, step), base, interleaved, dtype,
+                                           stream)
 
 
 def dsa3d_gated_ffn_workspace_bytes(rows, C, hidden, dtype) -> int:

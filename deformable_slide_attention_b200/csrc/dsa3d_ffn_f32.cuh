@@ -7,13 +7,13 @@
 // fp32 products stay fp32 here: the tensor cores' tf32 keeps 11 bits of each factor, and sums of split
 // bf16 factors are cut, not rounded, at every step of the accumulator.  The kernel is bound by the fp32
 // FMA pipes, or, at a few hundred tokens, by how many of them the tiles reach (backward of 1001 x 258 x
-// 685: 160 us, 18 TFLOP/s; 178 with tiles of 64 rows everywhere).  Tiles of 64 x 64 outputs (32 x 64 where those would
-// leave SMs idle), 16 along the summed axis, 4 x 4 sums per thread (8 x 4 leave a scheduler one warp: 253
-// us).  The next 16 are loaded into registers while these are
-// multiplied, by pointers that only move on, and two shared buffers make one barrier per step enough.
-// The products of one tile that the same outputs
-// need are formed by the same block (gate and up, and dWg and dWu, from one read of x; dh after them), and the activation, its
-// derivative and the element-wise products are the epilogue, so g, u and dh never reach memory.
+// 685: 160 us, 18 TFLOP/s; 178 with tiles of 64 rows everywhere).  Tiles of 64 x 64 outputs (32 x 64 where
+// those would leave SMs idle), 16 along the summed axis, 4 x 4 sums per thread (8 x 4 leave a scheduler one
+// warp: 253 us).  The next 16 are loaded into registers while these are multiplied, by pointers that only
+// move on, and two shared buffers make one barrier per step enough.  The products of one tile that the
+// same outputs need are formed by the same block (gate and up, and dWg and dWu, from one read of x; dh
+// after them), and the activation, its derivative and the element-wise products are the epilogue, so g, u
+// and dh never reach memory.
 #pragma once
 
 #include <stdint.h>

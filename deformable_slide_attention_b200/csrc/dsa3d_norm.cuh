@@ -254,7 +254,7 @@ __device__ __forceinline__ void ring_rows(Vec<T, V> (&v)[R][PER], const RowRing<
 // Block: TX * TY threads; group ty takes R consecutive rows per step.  nv = C / V vectors per row,
 // nv <= TX * PER.  The next step's rows are loaded into registers before this step's are reduced: the
 // two reductions and their barriers would otherwise leave HBM idle.  Bound by HBM where rows are wide:
-// 115,200 x 2048 bf16, residual sum included, 305 us (6.2 TB/s, 94% of a copy's rate; without the sum
+// 115,200 x 2048 bf16, residual sum included, 299 us (6.3 TB/s, 96% of a copy's rate; without the sum
 // 178 us, 81%: the element-wise work, halved by packed pairs, is then half the issue slots).
 template <typename T, int V, int PER, int R, bool ADD>
 __global__ void __launch_bounds__(norm_max_threads(PER, R)) dsa3d_layer_norm_kernel(

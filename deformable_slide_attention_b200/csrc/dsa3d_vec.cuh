@@ -20,7 +20,9 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 // For kernels launched early (launch_early): waits until the stream's previous kernel is complete and its
 // writes are visible; and, in that previous kernel, allows the next one's blocks to start.
 __device__ __forceinline__ void prior_kernel_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void next_kernel_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void next_kernel_may_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // Two fp32 values in 64 bits: one instruction for two sums, products or multiply-adds.
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
