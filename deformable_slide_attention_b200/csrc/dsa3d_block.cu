@@ -80,9 +80,10 @@ NormPlan norm_bwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype, bool add) {
   return p;
 }
 
-// Calls f with the plan's PER and R (and RING) as constants; V bounds PER (C <= kNormMaxChannels).
+// Calls f with the plan's PER and R (and RING) as constants; V bounds PER (C <= kNormMaxChannels), and whole
+// vectors go from two per thread to eight (two reach 1024 of them with the wide blocks).
 #define DSA3D_NORM_CASE(PER, R, RING)                                                                       \
-  if constexpr (PER <= (V == 1 ? 32 : kNormMaxChannels / (V * kNormThreads)) && (V > 1 || !RING))           \
+  if constexpr (PER <= (V == 1 ? 32 : kNormMaxChannels / (V * kNormThreads)) && (V > 1 ? PER != 4 : !RING)) \
     if (p.per == PER && p.r == R && p.ring == RING)                                                         \
       return f(std::integral_constant<int, PER>(), std::integral_constant<int, R>(), std::integral_constant<bool, RING>());
 template <int V, typename F>

@@ -654,7 +654,7 @@ dsa3d_status_t tc_backward(const Ffn& f, const FfnBwd& p, int64_t chunk, cudaStr
                         !result_map(&d.o[2], p.dwd, H, C, C)))
       return DSA3D_ERR_CUDA;
     d.a[1] = d.a[0];
-    if ((rc = tc_launch<kTcDw>(d, 2, st)) != DSA3D_OK) return rc;
+    if ((rc = tc_launch_cg<kTcDw, 2, 0>(d, st)) != DSA3D_OK) return rc;
   }
   return dw.units > dw.full ? tc_join(dw, 2, nullptr, p.dwg, p.dwu, p.dwd, st) : DSA3D_OK;
 }
