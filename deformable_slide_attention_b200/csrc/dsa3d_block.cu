@@ -68,8 +68,10 @@ NormPlan norm_fwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype) {
 NormPlan norm_bwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype, bool add) {
   NormPlan p = norm_plan(C, dtype, 4);
   const int64_t row = (int64_t)C * elem_size(dtype), sms = sm_count();
-  // short rows: steps of up to 8 KB per tensor (2,000,000 x 64 bf16: 141 us at four rows, 163 at one)
-  while (p.per == 1 && p.r < 4 && p.ty * p.r * 2 * row <= 8192 && ceil_div(rows, (int64_t)p.ty * p.r * 2) >= sms)
+  // short rows: steps of up to 16 KB per tensor, 8 KB of three (2,000,000 x 64 bf16: 141 us at four rows, 163
+  // at one)
+  const int64_t most = add ? 8192 : 16384;
+  while (p.per == 1 && p.r < 4 && p.ty * p.r * 2 * row <= most && ceil_div(rows, (int64_t)p.ty * p.r * 2) >= sms)
     p.r *= 2;
   // the ring: whole 16-byte rows, more steps than SMs (a block with one step has nothing to run ahead
   // of), and two blocks on an SM

@@ -27,7 +27,9 @@ def _randn(g, *shape, dtype=torch.float32, std=1.0, mean=0.0):
 
 # ---- layer norm --------------------------------------------------------------------------------------
 NORM_SHAPES = [(1, 1), (3, 2), (5, 7), (1, 8), (37, 32), (513, 64), (130, 100), (9, 258), (4099, 1001),
-               (777, 2048), (2500, 512), (33, 4096), (5, 8191), (7, 8200), (2, 16384), (0, 64)]
+               (777, 2048), (2500, 512), (33, 4096), (5, 8191), (7, 8200), (2, 16384), (0, 64),
+               # the backward's ring: four rows per step, blocks of 512 threads; element-wise rows, four in flight
+               (40000, 64), (400, 4096), (400, 8192), (150000, 5)]
 
 
 def _norm_inputs(rows, C, dtype, seed):
