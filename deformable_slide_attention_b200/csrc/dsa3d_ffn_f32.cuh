@@ -220,11 +220,11 @@ __global__ void __launch_bounds__(256) dsa3d_ffn_join_kernel(const __grid_consta
   prior_kernel_done();
   const int p = blockIdx.y;
   const int64_t n = r.n[p], step = (int64_t)gridDim.x * blockDim.x;
-  const float* __restrict__ from = r.partial[p];
+  const float* from = r.partial[p];
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += step) {
     float v = 0.f;
 #pragma unroll 4
-    for (int s = 0; s < r.parts; s++) v += __ldg(from + s * n + i);
+    for (int s = 0; s < r.parts; s++) v += from[s * n + i];
     if (r.add) v += r.add[i];
     r.out[p][i] = v;
   }

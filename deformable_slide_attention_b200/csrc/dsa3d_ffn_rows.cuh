@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kRowsThreads) dsa3d_ffn_rows_kernel(const __gr
           const int64_t up = (int64_t)a.rows * a.K;
 #pragma unroll 8
           for (int s = 0; s < a.in_parts; s++, p += 2 * up) {
-            g += __ldg(p);
-            u += __ldg(p + up);
+            g += p[0];
+            u += p[up];
           }
           float act, unused;
           f32_act(a.act, g, act, unused);
@@ -132,14 +132,14 @@ __global__ void __launch_bounds__(kRowsThreads) dsa3d_ffn_rows_kernel(const __gr
 
 // y[i] = sum_s partial[s][i] (+ add[i]), rounded once.
 template <typename T>
-__global__ void __launch_bounds__(256) dsa3d_ffn_rows_join_kernel(const float* __restrict__ partial, int parts,
+__global__ void __launch_bounds__(256) dsa3d_ffn_rows_join_kernel(const float* partial, int parts,
                                                                   const T* add, T* y, int n) {
   const int i = blockIdx.x * 256 + threadIdx.x;
   prior_kernel_done();
   if (i >= n) return;
   float v = 0.f;
 #pragma unroll 8
-  for (int s = 0; s < parts; s++) v += __ldg(partial + (int64_t)s * n + i);
+  for (int s = 0; s < parts; s++) v += partial[(int64_t)s * n + i];
   if (add) v += to_f32(add[i]);
   y[i] = from_f32<T>(v);
 }

@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(256) dsa3d_ffn_tail_kernel(const __grid_consta
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int p = 0; p < a.t.parts; p++) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(from + ((int64_t)p * a.tile_m + r) * 256));
+      const float4 x = *reinterpret_cast<const float4*>(from + ((int64_t)p * a.tile_m + r) * 256);
       v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
     }
     const int64_t at = (m0 + r) * N + n;

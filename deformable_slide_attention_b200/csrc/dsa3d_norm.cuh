@@ -512,9 +512,8 @@ __global__ void __launch_bounds__(norm_max_threads(PER, R)) dsa3d_layer_norm_bwd
 }
 
 // dw and db (each [C]) = the sum of P partial rows [2 C], in a fixed order.  Block 32 x 32: 32 columns.
-__global__ void __launch_bounds__(1024) dsa3d_norm_reduce_kernel(const float* __restrict__ partial, int P,
-                                                                 int C, float* __restrict__ dw,
-                                                                 float* __restrict__ db) {
+__global__ void __launch_bounds__(1024) dsa3d_norm_reduce_kernel(const float* partial, int P, int C, float* dw,
+                                                                 float* db) {
   __shared__ float s[32][33];
   const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
   const int64_t width = 2 * (int64_t)C;

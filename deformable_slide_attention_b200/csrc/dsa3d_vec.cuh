@@ -18,7 +18,9 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // For kernels launched early (launch_early): waits until the stream's previous kernel is complete and its
-// writes are visible; and, in that previous kernel, allows the next one's blocks to start.
+// writes are visible; and, in that previous kernel, allows the next one's blocks to start.  What the previous
+// kernel writes is not read-only for the life of one that starts early: it is read by ordinary loads after
+// the wait, never through __ldg or a const __restrict__ pointer (such loads may be moved over the wait).
 __device__ __forceinline__ void prior_kernel_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void next_kernel_may_start() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

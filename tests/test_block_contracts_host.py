@@ -1,0 +1,47 @@
+"""Contracts of the transformer block's operators that need no GPU: what kernels that start early may
+read how, workspace sizes, and refusals."""
+import glob
+import os
+import re
+
+import pytest
+
+from deformable_slide_attention_b200 import abi, build
+
+CSRC = os.path.join(os.path.dirname(build.__file__), "csrc")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+
+
+def _kernels():
+    """(name, parameters, body, file) of every __global__ function, comments removed."""
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu*"))):
+        with open(path) as f:
+            src = re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+        for m in re.finditer(r"__global__\s+void\s+(?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s+)?(\w+)\(", src):
+            at, depth = m.end(), 1
+            while depth:
+                depth += {"(": 1, ")": -1}.get(src[at], 0)
+                at += 1
+            begin = src.index("{", at)
+            end, depth = begin + 1, 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(src[end], 0)
+                end += 1
+            yield m.group(1), src[m.end():at - 1], src[begin:end], os.path.basename(path)
+
+
+def test_early_started_kernels_read_their_predecessors_data_by_ordinary_loads():
+    """A kernel that waits for its predecessor inside (prior_kernel_done) is resident while that one still
+    writes: its data is not read-only for the kernel's life, which __ldg and const __restrict__ promise, and
+    a load under that promise may be moved over the wait."""
+    early = [k for k in _kernels() if "prior_kernel_done()" in k[2]]
+    assert {k[0] for k in early} >= {"dsa3d_norm_reduce_kernel", "dsa3d_ffn_rows_kernel", "dsa3d_ffn_rows_join_kernel",
+                                     "dsa3d_ffn_join_kernel", "dsa3d_ffn_tail_kernel"}
+    for name, params, body, path in early:
+        after = body[body.index("prior_kernel_done()"):]
+        assert "__ldg(" not in after, (path, name)
+        assert not re.search(r"const\s+\w+\s*\*\s*__restrict__", params + body), (path, name)
