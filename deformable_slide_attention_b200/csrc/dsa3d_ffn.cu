@@ -27,6 +27,9 @@ using bf16 = __nv_bfloat16;
 constexpr int64_t kFfnChunk = 65536;    // tokens per chunk of a full-size workspace
 constexpr int64_t kFfnMinChunk = 256;   // and of the smallest one
 constexpr int kFfnMaxParts = 32;
+// Rounds of CTAs that the parts of a split tail may make (the costs below choose at most eight of their own
+// accord): the bound of the workspace for their sums.
+constexpr int kFfnTailRounds = 8;
 
 size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
@@ -66,6 +69,16 @@ int f32_out_parts(const Ffn& f, int64_t rows) { return f32_parts(tiles_for(rows,
 int f32_dw_parts(const Ffn& f, int64_t rows) {
   return f32_parts(2 * tiles_for(f.C, f.hidden, 64, kF32Cols), rows);
 }
+// Bounds of the split sums that no shorter call passes: the parts go down where the tiles fill the SMs,
+// and a workspace for many tokens has to be enough for few.  y and dx: parts * tiles stay within the slots.
+int64_t f32_out_sums(const Ffn& f, int64_t rows) {
+  const int64_t p = std::min<int64_t>(ceil_div(f.hidden, kF32K) / 8, kFfnMaxParts);
+  return p > 1 ? std::min(p * rows * f.C, 4 * (int64_t)sm_count() * 64 * kF32Cols) : 0;
+}
+int64_t f32_dw_max_parts(const Ffn& f, int64_t rows) {
+  const int64_t room = 4 * (int64_t)sm_count() / (2 * tiles_for(f.C, f.hidden, 64, kF32Cols));
+  return std::max<int64_t>(1, std::min<int64_t>({room, ceil_div(rows, kF32K) / 8, (int64_t)kFfnMaxParts}));
+}
 
 // CTAs per tensor-core tile: pairs, unless the rows fill no more than one CTA's 128.
 int tc_pair(int64_t rows) { return rows > 128 ? 2 : 1; }
@@ -92,7 +105,7 @@ FtTiles tc_tiles(int problems, const int64_t (&M)[3], const int64_t (&N)[3], int
   const double rounds = (double)ceil_div(tail, slots);
   double best = rounds;
   int64_t parts = 1;
-  for (int64_t p = 2; p <= kFfnMaxParts && p <= kblocks / 4 && tail < slots; p++) {
+  for (int64_t p = 2; p <= kFfnMaxParts && p <= kblocks / 4 && tail < slots && tail * p <= kFfnTailRounds * slots; p++) {
     if (ceil_div(kblocks, ceil_div(kblocks, p)) != p) continue;  // an empty part
     const double r = (double)ceil_div(tail * p, slots) / p + 0.01 * p;  // the parts' sums cross memory
     if (r < best) {
@@ -107,17 +120,36 @@ FtTiles tc_tiles(int problems, const int64_t (&M)[3], const int64_t (&N)[3], int
   t.units = t.full + (tiles - t.full) * parts;
   return t;
 }
-int64_t sums_elems(const FtTiles& t, int cg) { return (t.units - t.full) * 128 * cg * 256; }
+// A bound of the split sums of up to `tiles` tail tiles, which grows with the tiles and with the k-blocks.
+int64_t tc_sums(int64_t tiles, int64_t kblocks, int cg, bool all_tail) {
+  const int64_t tile = 128 * cg * 256, parts = std::min<int64_t>(kFfnMaxParts, kblocks / 4);
+  const int64_t split =
+      parts > 1 ? std::min(tiles * parts * tile, (int64_t)kFfnTailRounds * sm_count() * 128 * 256) : 0;
+  return all_tail ? std::max(split, tiles * tile) : split;
+}
 
 // y (one product) and dx (two): [rows][C] summed over hidden.
 FtTiles tc_out_tiles(const Ffn& f, int64_t rows, int products) {
   const int64_t M[3] = {rows}, N[3] = {f.C};
   return tc_tiles(1, M, N, tc_pair(rows), ceil_div(f.hidden, kFtK), products, f.ldc() != f.C);
 }
+int64_t tc_out_sums(const Ffn& f, int64_t rows) {
+  const int cg = tc_pair(rows);
+  return tc_sums(tiles_for(rows, f.C, 128 * cg, 256), ceil_div(f.hidden, kFtK), cg, f.ldc() != f.C);
+}
 // The three weight gradients, summed over tokens.
 FtTiles tc_dw_tiles(const Ffn& f, int64_t rows, bool all_tail) {
   const int64_t M[3] = {f.C, f.C, f.hidden}, N[3] = {f.hidden, f.hidden, f.C};
   return tc_tiles(3, M, N, 2, ceil_div(rows, kFtK), 1, all_tail);
+}
+// Their sums in chunks of `chunk` tokens.  Several chunks keep every tile's sums, a call of one chunk those
+// of its tail, which may be more: several chunks take the larger.
+int64_t tc_dw_sums(const Ffn& f, int64_t chunk) {
+  const int64_t tiles = 2 * tiles_for(f.C, f.hidden, 256, 256) + tiles_for(f.hidden, f.C, 256, 256);
+  const int64_t kblocks = ceil_div(chunk, kFtK), tail = tiles % std::max(1, sm_count() / 2);
+  const bool padded = f.ldc() != f.C || f.ldh() != f.hidden;
+  const int64_t all = chunk < f.rows || padded ? tc_sums(tiles, kblocks, 2, true) : 0;
+  return padded ? all : std::max(all, tc_sums(tail, kblocks, 2, false));
 }
 // The hidden values: tiles of tile_n columns, all whole.
 FtTiles tc_hidden_tiles(const Ffn& f, int64_t rows, int tile_n) {
@@ -166,14 +198,13 @@ struct FwdWs {
   char* h;                     // [chunk][ldw]; of few rows: y's parts (and sums: g's and u's)
   bf16 *x, *wg, *wu, *wd;      // copies with 16-byte rows, where the tensors have none
   float* sums;                 // y's split sums: fp32 [parts][chunk][C], bf16 the tail's tiles
-  size_t sums_elems, bytes;
+  size_t bytes;
 };
 FwdWs fwd_ws(const Ffn& f, int64_t chunk, void* base) {
   Carver c{static_cast<char*>(base)};
   FwdWs w{};
   if (few_rows(f)) {
-    w.sums_elems = (size_t)rows_parts(f, f.C, f.hidden) * 2 * f.rows * f.hidden;
-    w.sums = c.take<float>(true, w.sums_elems);
+    w.sums = c.take<float>(true, (size_t)rows_parts(f, f.C, f.hidden) * 2 * f.rows * f.hidden);
     w.h = c.take<char>(true, (size_t)rows_parts(f, f.hidden, f.C) * f.rows * f.C * sizeof(float));
     w.bytes = c.used;
     return w;
@@ -184,13 +215,8 @@ FwdWs fwd_ws(const Ffn& f, int64_t chunk, void* base) {
   w.wg = c.take<bf16>(padh, (size_t)f.C * f.ldh());
   w.wu = c.take<bf16>(padh, (size_t)f.C * f.ldh());
   w.wd = c.take<bf16>(padc, (size_t)f.hidden * f.ldc());
-  if (f.f32()) {
-    const int parts = f32_out_parts(f, chunk);
-    w.sums_elems = parts > 1 ? (size_t)parts * chunk * f.C : 0;
-  } else {
-    w.sums_elems = (size_t)sums_elems(tc_out_tiles(f, chunk, 1), tc_pair(chunk));
-  }
-  w.sums = c.take<float>(w.sums_elems > 0, w.sums_elems);
+  const size_t sums = (size_t)(f.f32() ? f32_out_sums(f, chunk) : tc_out_sums(f, chunk));
+  w.sums = c.take<float>(sums > 0, sums);
   w.bytes = c.used;
   return w;
 }
@@ -200,7 +226,7 @@ struct BwdWs {
   bf16 *x, *dy, *wg, *wu, *wd;      // copies with 16-byte rows
   float* dw[3];                     // the weight gradients' split sums (bf16: dw[0], the tail's tiles of all three)
   float* sums;                      // dx's
-  size_t sums_elems, bytes;
+  size_t bytes;
   bool dw_sums;                     // fp32: the weight gradients go through dw
 };
 // bf16 weight gradients whose sums all go through the workspace: several chunks, or rows TMA cannot store.
@@ -223,20 +249,26 @@ BwdWs bwd_ws(const Ffn& f, int64_t chunk, void* base) {
   w.dw_sums = false;
   w.dw[0] = w.dw[1] = w.dw[2] = nullptr;
   if (f.f32()) {
-    const int dparts = f32_dw_parts(f, chunk), parts = f32_out_parts(f, chunk);
-    w.dw_sums = dparts > 1 || chunk < f.rows;
-    for (int i = 0; i < 3; i++) w.dw[i] = c.take<float>(w.dw_sums, (size_t)dparts * f.C * f.hidden);
-    w.sums_elems = parts > 1 ? (size_t)parts * chunk * f.C : 0;
+    w.dw_sums = f32_dw_parts(f, chunk) > 1 || chunk < f.rows;
+    const int64_t parts = f32_dw_max_parts(f, chunk);
+    const bool room = parts > 1 || chunk < f.rows;
+    for (int i = 0; i < 3; i++) w.dw[i] = c.take<float>(room, (size_t)parts * f.C * f.hidden);
   } else {
-    const size_t n = (size_t)sums_elems(tc_dw_tiles(f, chunk, dw_all_tail(f, chunk)), 2);
+    const size_t n = (size_t)tc_dw_sums(f, chunk);
     w.dw[0] = c.take<float>(n > 0, n);
-    w.sums_elems = (size_t)sums_elems(tc_out_tiles(f, chunk, 2), tc_pair(chunk));
   }
-  w.sums = c.take<float>(w.sums_elems > 0, w.sums_elems);
+  const size_t sums = (size_t)(f.f32() ? f32_out_sums(f, chunk) : tc_out_sums(f, chunk));
+  w.sums = c.take<float>(sums > 0, sums);
   w.bytes = c.used;
   return w;
 }
-size_t fwd_bytes(const Ffn& f, int64_t chunk) { return fwd_ws(f, chunk, nullptr).bytes; }
+// Grows with the chunk; a call past the few-token path asks for no less than that path's longest.
+size_t fwd_bytes(const Ffn& f, int64_t chunk) {
+  const size_t own = fwd_ws(f, chunk, nullptr).bytes;
+  Ffn few = f;
+  few.rows = std::min<int64_t>(f.rows, f.f32() ? kRowsMaxF32 : kRowsMaxBf16);
+  return few_rows(few) ? std::max(own, fwd_ws(few, few.rows, nullptr).bytes) : own;
+}
 size_t bwd_bytes(const Ffn& f, int64_t chunk) { return bwd_ws(f, chunk, nullptr).bytes; }
 
 // A chunk whose workspace fits: all rows, or a multiple of kFfnMinChunk; 0 when none does.
@@ -567,18 +599,10 @@ dsa3d_status_t tc_join(const FtTiles& t, int cg, const bf16* add, void* o0, void
 
 // y or dx: one launch, and the joining of its tail where it has one.
 template <int MODE>
-dsa3d_status_t tc_out(const Ffn& f, FtArgs& a, int64_t n, const float* sums, size_t sums_have, const bf16* add,
-                      bf16* out, cudaStream_t st) {
+dsa3d_status_t tc_out(const Ffn& f, FtArgs& a, int64_t n, float* sums, const bf16* add, bf16* out, cudaStream_t st) {
   const int cg = tc_pair(n);
   a.t = tc_out_tiles(f, n, MODE == kTcDx ? 2 : 1);
-  if ((size_t)sums_elems(a.t, cg) > sums_have) {
-    // a last, shorter chunk whose tail would be larger than the others': no cutting
-    a.t.parts = 1;
-    a.t.per_part = a.t.kblocks;
-    a.t.full = f.ldc() != f.C ? 0 : a.t.tiles_of[0];
-    a.t.units = a.t.tiles_of[0];
-  }
-  a.t.sums = const_cast<float*>(sums);
+  a.t.sums = sums;  // room for a whole chunk's (tc_out_sums), and so for a shorter one's
   a.add = add;
   if (a.t.full > 0 && !result_map(&a.o[0], out, n, f.C, f.C)) return DSA3D_ERR_CUDA;
   const dsa3d_status_t rc = tc_launch<MODE>(a, cg, st);
@@ -605,7 +629,7 @@ dsa3d_status_t tc_forward(const Ffn& f, const FfnFwd& p, int64_t chunk, cudaStre
     if ((rc = tc_launch_gated<kTcHidden>(a, tc_pair(n), f.act, st)) != DSA3D_OK) return rc;
     FtArgs b{};
     if (!k_major_map(&b.a[0], w.h, n, H, lw, 128) || !mn_major_map(&b.b[0], wd, H, C, lc)) return DSA3D_ERR_CUDA;
-    rc = tc_out<kTcOut>(f, b, n, w.sums, w.sums_elems, at_row<bf16>(p.add, r0, C), at_row<bf16>(p.y, r0, C), st);
+    rc = tc_out<kTcOut>(f, b, n, w.sums, at_row<bf16>(p.add, r0, C), at_row<bf16>(p.y, r0, C), st);
     if (rc != DSA3D_OK) return rc;
   }
   return DSA3D_OK;
@@ -639,7 +663,7 @@ dsa3d_status_t tc_backward(const Ffn& f, const FfnBwd& p, int64_t chunk, cudaStr
     if (!k_major_map(&b.a[0], w.dg, n, H, lw, 128) || !k_major_map(&b.a[1], w.du, n, H, lw, 128) ||
         !k_major_map(&b.b[0], wg, C, H, lh, 256 / cg) || !k_major_map(&b.b[1], wu, C, H, lh, 256 / cg))
       return DSA3D_ERR_CUDA;
-    rc = tc_out<kTcDx>(f, b, n, w.sums, w.sums_elems, nullptr, at_row<bf16>(p.dx, r0, C), st);
+    rc = tc_out<kTcDx>(f, b, n, w.sums, nullptr, at_row<bf16>(p.dx, r0, C), st);
     if (rc != DSA3D_OK) return rc;
     FtArgs d{};
     d.t = dw;

@@ -339,7 +339,8 @@ dsa3d_status_t dsa3d_rotary3d_backward(const void *dq_out, const void *dk_out, v
  * multiple of 8 through copies with padded rows in the workspace), fp32 on CUDA cores in fp32.
  * The workspace holds a chunk of tokens' hidden values; the size dsa3d_gated_ffn_workspace_bytes
  * returns covers min(rows, 65536) tokens, and any workspace of at least the size for min(rows, 256)
- * works (tokens are then processed in more chunks).  The sizes depend on the current device.
+ * works (tokens are then processed in more chunks).  The sizes never go down with rows (one workspace for
+ * the longest call serves every shorter one) and depend on the current device.
  */
 typedef enum { DSA3D_SILU = 0, DSA3D_GELU = 1 } dsa3d_activation_t;
 

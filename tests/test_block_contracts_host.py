@@ -45,3 +45,23 @@ def test_early_started_kernels_read_their_predecessors_data_by_ordinary_loads():
         after = body[body.index("prior_kernel_done()"):]
         assert "__ldg(" not in after, (path, name)
         assert not re.search(r"const\s+\w+\s*\*\s*__restrict__", params + body), (path, name)
+
+
+# C, hidden: few-token paths (16-byte rows), odd widths, summed axes long enough to be cut
+WORKSPACE_WIDTHS = [(4096, 10944), (2048, 8192), (512, 2048), (64, 136), (61, 131), (1001, 4099)]
+
+
+def check_workspace_never_shrinks(C, hidden, dtype):
+    """A workspace sized once for the longest call is enough for every shorter one."""
+    rows = sorted({*range(0, 20), 100, 127, 128, 129, 255, 256, 257, *range(300, 5000, 97), *range(512, 20000, 256),
+                   *range(20000, 65536, 2999), 65280, 65535, 65536, 65537, 100000, 1 << 21, (1 << 31) - 1})
+    for size in (abi.dsa3d_gated_ffn_workspace_bytes, abi.dsa3d_gated_ffn_backward_workspace_bytes):
+        sizes = [size(r, C, hidden, dtype) for r in rows]
+        for i in range(1, len(rows)):
+            assert sizes[i] >= sizes[i - 1], (size.__name__, rows[i - 1], sizes[i - 1], rows[i], sizes[i])
+
+
+@pytest.mark.parametrize("dtype", [abi.DSA3D_F32, abi.DSA3D_BF16])
+@pytest.mark.parametrize("C,hidden", WORKSPACE_WIDTHS)
+def test_feed_forward_workspace_never_shrinks(C, hidden, dtype):
+    check_workspace_never_shrinks(C, hidden, dtype)
