@@ -85,3 +85,10 @@ def test_gated_ffn_f32_in_chunks_with_split_sums(tokens):
     size = abi.dsa3d_gated_ffn_backward_workspace_bytes(tokens, C, hidden, abi.DSA3D_F32)
     ws = torch.empty(size + 12 * 256 * 1280 + 1024, dtype=torch.uint8, device="cuda")
     _check_grads(abi.gated_ffn_backward(x, *w, dy, workspace=ws), ref.gated_ffn_backward(x, *w, dy, "silu"))
+
+
+# ---- last: the device's record ----------------------------------------------------------------------------
+def test_no_wait_ran_out_in_any_test_before():
+    """Nothing that ran since the record was last read (streams, graphs and chunks among it) gave up a wait."""
+    torch.cuda.synchronize()
+    assert abi.dsa3d_check_device(torch.cuda.current_stream().cuda_stream) == 0
