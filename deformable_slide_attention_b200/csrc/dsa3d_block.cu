@@ -252,7 +252,8 @@ dsa3d_status_t rotary(const void* q, const void* k, void* qo, void* ko, long lon
   if (!q || !qo || (k == nullptr) != (ko == nullptr)) return DSA3D_ERR_INVALID_ARGUMENT;
   const size_t es = elem_size(dtype);
   if (ldq < width || ldqo < width || (k && (ldk < width || ldko < width))) return DSA3D_ERR_INVALID_ARGUMENT;
-  const long long most = 1LL << 40;  // token strides whose product with the rows stays in 64 bits
+  // token strides whose product with the rows is an offset of 64 bits, in bytes too
+  const long long most = std::min<long long>(1LL << 40, (1LL << 60) / rows);
   if (ldq > most || ldqo > most || (k && (ldk > most || ldko > most))) return DSA3D_ERR_UNSUPPORTED;
   const void* al[4] = {q, k, qo, ko};
   for (const void* p : al)

@@ -65,3 +65,28 @@ def check_workspace_never_shrinks(C, hidden, dtype):
 @pytest.mark.parametrize("C,hidden", WORKSPACE_WIDTHS)
 def test_feed_forward_workspace_never_shrinks(C, hidden, dtype):
     check_workspace_never_shrinks(C, hidden, dtype)
+
+
+# ---- refusals (fake, 16-byte aligned addresses: validation fails before any device access) -----------------
+INV, UNS = 1, 2
+ROT = dict(first=0, rows=24, F=2, Hp=3, Wp=4, heads=2, dh=32, axes=(12, 10, 10), start=(0.0,) * 3, step=(1.0,) * 3,
+           base=10000.0, ld=(64,) * 4, p=tuple((i + 1) << 40 for i in range(4)))
+
+
+def rotary(fn, **kw):
+    a = {**ROT, **kw}
+    return fn(*a["p"], *a["ld"], a["first"], a["rows"], a["F"], a["Hp"], a["Wp"], a["heads"], a["dh"], a["axes"],
+              a["start"], a["step"], a["base"], 1, abi.DSA3D_BF16, 0)
+
+
+@pytest.mark.parametrize("fn", [abi.dsa3d_rotary3d, abi.dsa3d_rotary3d_backward])
+def test_rotary_strides_whose_product_with_the_rows_passes_64_bits_are_refused(fn):
+    """Offsets are 64-bit sums: (2^31 - 1) tokens 2^40 elements apart would wrap around them."""
+    grid = dict(F=1 << 15, Hp=1 << 8, Wp=255)
+    rows = grid["F"] * grid["Hp"] * grid["Wp"]
+    for i in range(4):
+        ld = [64] * 4
+        ld[i] = 1 << 40
+        assert rotary(fn, **grid, rows=rows, ld=tuple(ld)) == UNS, i
+    assert rotary(fn, **grid, rows=rows, ld=(1 << 33,) * 4) == UNS
+    assert rotary(fn, **grid, rows=rows, ld=(64, 1 << 31, 64, 64)) == UNS
