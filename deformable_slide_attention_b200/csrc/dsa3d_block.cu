@@ -245,9 +245,11 @@ dsa3d_status_t rotary(const void* q, const void* k, void* qo, void* ko, long lon
   if (R < 2 || R > dh) return DSA3D_ERR_INVALID_ARGUMENT;
   if (!(base > 0.0) || !std::isfinite(base)) return DSA3D_ERR_INVALID_ARGUMENT;
   const int dims[3] = {F, Hp, Wp};
-  for (int i = 0; i < 3; i++)  // positions the fp64 angle can reduce
-    if (!(std::fabs(start[i]) + std::fabs(step[i]) * dims[i] <= 1099511627776.0))
-      return DSA3D_ERR_INVALID_ARGUMENT;
+  for (int i = 0; i < 3; i++) {  // angles that fp64 can reduce; below a base of 1 the last pair turns fastest
+    const double most = std::fabs(start[i]) + std::fabs(step[i]) * dims[i];
+    const double fastest = base < 1.0 && axes[i] > 2 ? std::pow(base, -(axes[i] - 2.0) / axes[i]) : 1.0;
+    if (!(most <= 1099511627776.0) || !(most * fastest <= 1099511627776.0)) return DSA3D_ERR_INVALID_ARGUMENT;
+  }
   if (rows == 0) return DSA3D_OK;
   if (!q || !qo || (k == nullptr) != (ko == nullptr)) return DSA3D_ERR_INVALID_ARGUMENT;
   const size_t es = elem_size(dtype);

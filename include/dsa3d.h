@@ -313,8 +313,8 @@ dsa3d_status_t dsa3d_layer_norm_backward(const void *h, const float *weight, con
  *   projection, and written into one).  Pointers are aligned to their elements here; 16-byte aligned
  *   pointers, strides and heads take the vector kernel.  q_out may be q, and k_out k, with the same
  *   stride (in place); k and k_out may both be NULL.  axes, start and step are host arrays.
- * dh even, 2..256; F*Hp*Wp < 2^31; |start| + |step| * extent <= 2^40; token strides <= 2^40 and
- * rows * stride <= 2^60.
+ * dh even, 2..256; F*Hp*Wp < 2^31; |start| + |step| * extent <= 2^40, with a base below 1 also its
+ * product with the axis's largest frequency; token strides <= 2^40 and rows * stride <= 2^60.
  */
 dsa3d_status_t dsa3d_rotary3d(const void *q, const void *k, void *q_out, void *k_out, long long ldq,
                               long long ldk, long long ldqo, long long ldko, long long first,

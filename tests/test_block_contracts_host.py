@@ -90,3 +90,15 @@ def test_rotary_strides_whose_product_with_the_rows_passes_64_bits_are_refused(f
         assert rotary(fn, **grid, rows=rows, ld=tuple(ld)) == UNS, i
     assert rotary(fn, **grid, rows=rows, ld=(1 << 33,) * 4) == UNS
     assert rotary(fn, **grid, rows=rows, ld=(64, 1 << 31, 64, 64)) == UNS
+
+
+@pytest.mark.parametrize("fn", [abi.dsa3d_rotary3d, abi.dsa3d_rotary3d_backward])
+def test_rotary_bases_below_one_whose_angles_cannot_be_reduced_are_refused(fn):
+    """Below a base of 1 frequencies grow with the pair: base^(-10/12) for the last of 12 dims.  Positions
+    times the largest frequency stay within the 2^40 that positions alone do; past it fp64 keeps no angle, and
+    frequencies of infinity would give NaN."""
+    for base in (1e-300, 5e-324, 1e-30):
+        assert rotary(fn, base=base) == INV, base
+    far = (2.0 ** 39, 0.0, 0.0)
+    assert rotary(fn, base=0.1, start=far) == INV
+    assert rotary(fn, base=1e-300, axes=(0, 2, 12)) == INV

@@ -87,6 +87,17 @@ def test_gated_ffn_f32_in_chunks_with_split_sums(tokens):
     _check_grads(abi.gated_ffn_backward(x, *w, dy, workspace=ws), ref.gated_ffn_backward(x, *w, dy, "silu"))
 
 
+# ---- rotary positions ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("backward", [False, True])
+@pytest.mark.parametrize("base", [0.25, 1.0, 2.0])
+def test_rotary_bases_near_one(base, backward):
+    q = _randn(_gen(3), 60, 2, 64)
+    kw = dict(first=0, start=(1000.0, 0.0, -3.5), step=(1.0, 0.5, 2.0), base=base, interleaved=True)
+    call = abi.rotary3d_backward if backward else abi.rotary3d
+    got, _ = call(q, None, (3, 4, 5), (16, 24, 24), **kw)
+    check("q", got, *ref.rotary(q, (3, 4, 5), (16, 24, 24), backward=backward, **kw))
+
+
 # ---- last: the device's record ----------------------------------------------------------------------------
 def test_no_wait_ran_out_in_any_test_before():
     """Nothing that ran since the record was last read (streams, graphs and chunks among it) gave up a wait."""
