@@ -314,7 +314,8 @@ dsa3d_status_t dsa3d_layer_norm(const void* x, const void* add, const float* wei
   if (!(eps >= 0.f) || !std::isfinite(eps)) return DSA3D_ERR_INVALID_ARGUMENT;
   if (rows == 0) return DSA3D_OK;
   if (!x || !y || (add == nullptr) != (h == nullptr) || (bias && !weight)) return DSA3D_ERR_INVALID_ARGUMENT;
-  if (!aligned16(x) || !aligned16(add) || !aligned16(y) || !aligned16(h) || !aligned(weight, 4) ||
+  const unsigned al = row_alignment(C, dtype);
+  if (!aligned(x, al) || !aligned(add, al) || !aligned(y, al) || !aligned(h, al) || !aligned(weight, 4) ||
       !aligned(bias, 4) || !aligned(stats, 4))
     return DSA3D_ERR_INVALID_ARGUMENT;
   const size_t tb = (size_t)rows * C * elem_size(dtype), wb = (size_t)C * 4;
@@ -357,7 +358,8 @@ dsa3d_status_t dsa3d_layer_norm_backward(const void* h, const float* weight, con
     return DSA3D_OK;
   }
   if (!h || !stats || !dy || !dx) return DSA3D_ERR_INVALID_ARGUMENT;
-  if (!aligned16(h) || !aligned16(dy) || !aligned16(add) || !aligned16(dx) || !aligned(stats, 4) ||
+  const unsigned al = row_alignment(C, dtype);
+  if (!aligned(h, al) || !aligned(dy, al) || !aligned(add, al) || !aligned(dx, al) || !aligned(stats, 4) ||
       !aligned16(workspace))
     return DSA3D_ERR_INVALID_ARGUMENT;
   const size_t need = weight ? norm_bwd_ws_bytes(rows, C, dtype) : 0;

@@ -54,6 +54,14 @@ dsa3d_status_t check_ffn_shape(long long rows, int C, int hidden, dsa3d_dtype_t 
   return DSA3D_OK;
 }
 
+// Tensors whose rows have n elements.
+template <size_t K>
+bool rows_aligned(const void* const (&tensors)[K], int64_t n, dsa3d_dtype_t dtype) {
+  for (const void* p : tensors)
+    if (!aligned(p, row_alignment(n, dtype))) return false;
+  return true;
+}
+
 // --- plan: parts of a summed axis, and the workspace -------------------------------------------------
 int64_t tiles_for(int64_t m, int64_t n, int tile_m, int tile_n) { return ceil_div(m, tile_m) * ceil_div(n, tile_n); }
 
@@ -714,9 +722,9 @@ dsa3d_status_t dsa3d_gated_ffn(const void* x, const void* gate_weight, const voi
   if (activation != DSA3D_SILU && activation != DSA3D_GELU) return DSA3D_ERR_INVALID_ARGUMENT;
   if (rows == 0) return DSA3D_OK;
   if (!x || !gate_weight || !up_weight || !down_weight || !y || !workspace) return DSA3D_ERR_INVALID_ARGUMENT;
-  const void* al[] = {x, gate_weight, up_weight, down_weight, add, y, workspace};
-  for (const void* p : al)
-    if (!aligned16(p)) return DSA3D_ERR_INVALID_ARGUMENT;
+  const void *by_c[] = {x, down_weight, add, y}, *by_hidden[] = {gate_weight, up_weight};
+  if (!rows_aligned(by_c, C, dtype) || !rows_aligned(by_hidden, hidden, dtype) || !aligned16(workspace))
+    return DSA3D_ERR_INVALID_ARGUMENT;
   const Ffn f{rows, C, hidden, activation == DSA3D_SILU ? kActSilu : kActGelu, dtype};
   const size_t tb = (size_t)rows * C * f.es(), wb = (size_t)C * hidden * f.es();
   const Range ry = range_of(y, tb), rw = range_of(workspace, workspace_bytes);
@@ -754,9 +762,10 @@ dsa3d_status_t dsa3d_gated_ffn_backward(const void* x, const void* gate_weight, 
   if (!gate_weight || !up_weight || !down_weight || !dgate_weight || !dup_weight || !ddown_weight)
     return DSA3D_ERR_INVALID_ARGUMENT;
   if (rows > 0 && (!x || !dy || !dx || !workspace)) return DSA3D_ERR_INVALID_ARGUMENT;
-  const void* al[] = {x, gate_weight, up_weight, down_weight, dy, dx, dgate_weight, dup_weight, ddown_weight, workspace};
-  for (const void* p : al)
-    if (!aligned16(p)) return DSA3D_ERR_INVALID_ARGUMENT;
+  const void *by_c[] = {x, down_weight, dy, dx, ddown_weight};
+  const void* by_hidden[] = {gate_weight, up_weight, dgate_weight, dup_weight};
+  if (!rows_aligned(by_c, C, dtype) || !rows_aligned(by_hidden, hidden, dtype) || !aligned16(workspace))
+    return DSA3D_ERR_INVALID_ARGUMENT;
   const Range ins[] = {range_of(x, tb), range_of(dy, tb), range_of(gate_weight, wb), range_of(up_weight, wb),
                        range_of(down_weight, wb)};
   const Range outs[] = {range_of(dx, tb), range_of(dgate_weight, wb), range_of(dup_weight, wb),

@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
@@ -18,6 +19,13 @@ inline bool aligned(const void* p, unsigned to) { return (reinterpret_cast<uintp
 inline bool aligned16(const void* p) { return aligned(p, 16); }
 inline size_t elem_size(dsa3d_dtype_t t) { return t == DSA3D_F32 ? 4 : 2; }
 inline bool known(dsa3d_dtype_t t) { return t == DSA3D_F32 || t == DSA3D_BF16; }
+// Alignment of a tensor whose rows have n elements: 16 bytes, or where rows are no multiple of them what every
+// row of a 16-byte aligned tensor keeps, so that a shard may start at any row.  The kernels load such rows by
+// pieces of that size at most.
+inline unsigned row_alignment(int64_t n, dsa3d_dtype_t t) {
+  const uint64_t bytes = (uint64_t)n * elem_size(t);
+  return (unsigned)std::min<uint64_t>(16, bytes & (~bytes + 1));
+}
 
 struct Range {
   uintptr_t lo, hi;

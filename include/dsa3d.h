@@ -266,6 +266,9 @@ dsa3d_status_t dsa3d_offset_head(const void *x, const float *dw_weight, const fl
  * an MLP, layer norm and residual sums): layer norm, rotary positions of the token grid for q and k,
  * and a gated feed-forward block, each with its backward pass.  Rows are tokens; rows = 0 is a valid
  * empty call (weight gradients are then zero, everything else is left alone).
+ * Alignment: workspaces 16 bytes, the norm's fp32 vectors and stats 4.  The norm's and the feed-forward
+ * block's other tensors 16 bytes or, where their rows are no multiple of that, the largest power of two that
+ * divides a row's bytes: any row of an aligned tensor may be a call's first.
  */
 
 /*

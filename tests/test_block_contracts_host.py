@@ -102,3 +102,35 @@ def test_rotary_bases_below_one_whose_angles_cannot_be_reduced_are_refused(fn):
     far = (2.0 ** 39, 0.0, 0.0)
     assert rotary(fn, base=0.1, start=far) == INV
     assert rotary(fn, base=1e-300, axes=(0, 2, 12)) == INV
+
+
+def _at(i):
+    return (i + 1) << 40
+
+
+def test_alignment_follows_the_rows():
+    """16 bytes, or what the rows of a tensor keep (a shard that starts at any of them): less is refused."""
+    p = [_at(i) for i in range(7)]  # x, add, weight, bias, y, h, stats
+    for C, dtype, less in ((61, abi.DSA3D_BF16, 1), (62, abi.DSA3D_BF16, 2), (60, abi.DSA3D_BF16, 4),
+                           (64, abi.DSA3D_BF16, 8), (61, abi.DSA3D_F32, 2), (62, abi.DSA3D_F32, 4),
+                           (64, abi.DSA3D_F32, 8)):
+        for i in (0, 1, 4, 5):
+            q = list(p)
+            q[i] += less
+            assert abi.dsa3d_layer_norm(*q, 10, C, 1e-5, dtype, 0) == INV, (C, dtype, i)
+        b = [_at(i) for i in range(9)]  # h, weight, stats, dy, add, dx, dw, db, ws
+        for i in (0, 3, 4, 5):
+            q = list(b)
+            q[i] += less
+            assert abi.dsa3d_layer_norm_backward(*q, 1 << 30, 10, C, dtype, 0) == INV, (C, dtype, i)
+        f = [_at(i) for i in range(7)]  # x, wg, wu, wd, add, y, ws
+        for i, widths in ((0, (C, 64)), (3, (C, 64)), (4, (C, 64)), (5, (C, 64)), (1, (64, C)), (2, (64, C)), (6, (64, C))):
+            q = list(f)
+            q[i] += 8 if i == 6 else less
+            assert abi.dsa3d_gated_ffn(*q, 1 << 30, 10, *widths, 0, dtype, 0) == INV, (C, dtype, i)
+        f = [_at(i) for i in range(10)]  # x, wg, wu, wd, dy, dx, dwg, dwu, dwd, ws
+        for i, widths in ((0, (C, 64)), (3, (C, 64)), (4, (C, 64)), (5, (C, 64)), (8, (C, 64)), (1, (64, C)), (2, (64, C)),
+                          (6, (64, C)), (7, (64, C)), (9, (64, C))):
+            q = list(f)
+            q[i] += 8 if i == 9 else less
+            assert abi.dsa3d_gated_ffn_backward(*q, 1 << 30, 10, *widths, 0, dtype, 0) == INV, (C, dtype, i)

@@ -98,6 +98,50 @@ def test_rotary_bases_near_one(base, backward):
     check("q", got, *ref.rotary(q, (3, 4, 5), (16, 24, 24), backward=backward, **kw))
 
 
+# ---- shards of tensors whose rows are no multiple of 16 bytes -------------------------------------------------
+def _shard(t, first):
+    """The rows from `first` on, where they lie; the same values in a tensor of their own."""
+    return t[first:], t[first:].clone()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [5, 61, 62, 60, 1001])
+@pytest.mark.parametrize("first", [1, 2, 3])
+def test_layer_norm_of_a_shard_of_odd_rows(C, first, dtype):
+    td = DT[dtype]
+    g = _gen(C * 4 + first)
+    (x, x0), (a, a0), (dy, dy0), (out, _) = (_shard(_randn(g, 50 + first, C, dtype=td), first) for _ in range(4))
+    w, b = _randn(g, C), _randn(g, C)
+    y, h, stats = abi.layer_norm(x, w, b, add=a, out=out)
+    assert y.data_ptr() == out.data_ptr()
+    (ry, rh, rs), (ey, es) = ref.layer_norm(x0, w, b, 1e-5, a0)
+    check("y", y, ry, ey)
+    check("stats", stats, rs, es)
+    assert torch.equal(h, rh)
+    got = abi.layer_norm_backward(x, w, stats, dy, add=a)
+    want, bound = ref.layer_norm_backward(x0, w, stats, dy0, a0)
+    for name, o, r, e in zip(("dx", "dw", "db"), got, want, bound):
+        check(name, o, r, e)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C,hidden", [(61, 131), (62, 130), (60, 132), (60, 64), (64, 131)])
+@pytest.mark.parametrize("rows", [1, 140])
+def test_gated_ffn_of_shards_of_odd_rows(rows, C, hidden, dtype):
+    """Every tensor starts at the second row of a larger one (of 16-byte rows that changes nothing)."""
+    td = DT[dtype]
+    shards = [_shard(t, 1) for t in (lambda x, w, a, dy: (x, *w, a, dy))(*_ffn_inputs(rows + 1, C, hidden, td, rows))]
+    x, wg, wu, wd, a, dy = (t for t, _ in shards)
+    w = [_shard(torch.cat([t[:1], t, t[:1]]), 1)[0][:n] for t, n in ((wg, C), (wu, C), (wd, hidden))]
+    own = [t.clone() for t in (x, *w, a, dy)]
+    out = torch.zeros(rows + 1, C, dtype=td, device="cuda")
+    y = abi.gated_ffn(x, *w, add=a, out=out[1:])
+    check("y", y, *ref.gated_ffn(own[0], *own[1:4], "silu", own[4]))
+    assert not out[0].any()
+    got = abi.gated_ffn_backward(x, *w, dy)
+    _check_grads(got, ref.gated_ffn_backward(own[0], *own[1:4], own[5], "silu"))
+
+
 # ---- last: the device's record ----------------------------------------------------------------------------
 def test_no_wait_ran_out_in_any_test_before():
     """Nothing that ran since the record was last read (streams, graphs and chunks among it) gave up a wait."""
