@@ -68,11 +68,10 @@ NormPlan norm_fwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype) {
 NormPlan norm_bwd_plan(int64_t rows, int C, dsa3d_dtype_t dtype, bool add) {
   NormPlan p = norm_plan(C, dtype, 4);
   const int64_t row = (int64_t)C * elem_size(dtype), sms = sm_count();
-  // short rows: steps of up to 16 KB per tensor, 8 KB of three (2,000,000 x 64 bf16: 141 us at four rows, 163
-  // at one)
-  const int64_t most = add ? 8192 : 16384;
-  while (p.per == 1 && p.r < 4 && p.ty * p.r * 2 * row <= most && ceil_div(rows, (int64_t)p.ty * p.r * 2) >= sms)
-    p.r *= 2;
+  // short rows, several per step: up to four (2,000,000 x 64 bf16: 141 us at four rows, 163 at one), two of three
+  // tensors in whole vectors (4 to 8 KB of each per step, and the ring holds three steps)
+  const int most = add && p.v > 1 ? 2 : 4;
+  while (p.per == 1 && p.r < most && ceil_div(rows, (int64_t)p.ty * p.r * 2) >= sms) p.r *= 2;
   // the ring: whole 16-byte rows, more steps than SMs (a block with one step has nothing to run ahead
   // of), and two blocks on an SM
   p.smem = (size_t)kRing * (add ? 3 : 2) * p.ty * p.r * row;
@@ -146,8 +145,10 @@ dsa3d_status_t norm_bwd(const NormBwd& a, const NormPlan& p, cudaStream_t st) {
   return norm_bwd_dispatch<V>(p, [&](auto per, auto r, auto ring) {
     constexpr int PER = decltype(per)::value, R = decltype(r)::value;
     constexpr bool RING = decltype(ring)::value;
-    auto* kern = a.add ? dsa3d_layer_norm_bwd_kernel<T, V, PER, R, true, RING>
-                       : dsa3d_layer_norm_bwd_kernel<T, V, PER, R, false, RING>;
+    auto* kern = dsa3d_layer_norm_bwd_kernel<T, V, PER, R, false, RING>;
+    if constexpr (V == 1 || R < 4) {  // four rows of whole vectors: never with an add
+      if (a.add) kern = dsa3d_layer_norm_bwd_kernel<T, V, PER, R, true, RING>;
+    }
     if (!norm_smem(kern, p)) return DSA3D_ERR_CUDA;
     return launch(kKernLayerNormBwd, st, [&] {
       kern<<<p.blocks, p.tx * p.ty, p.smem, st>>>(
