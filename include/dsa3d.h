@@ -339,8 +339,10 @@ dsa3d_status_t dsa3d_rotary3d_backward(const void *dq_out, const void *dk_out, v
  *   down_weight Wd [hidden][C], all in the I/O type;  act: silu(g) = g / (1 + e^-g), or gelu(g) =
  *   g Phi(g) with the normal distribution Phi (erf, not the tanh form).
  * Sums are fp32; act(x Wg) * (x Wu) is rounded to the I/O type once, as the operand of the second
- * product.  rows < 2^31, C and hidden <= 2^20.  bf16 runs on the tensor cores (widths that are no
- * multiple of 8 through copies with padded rows in the workspace), fp32 on CUDA cores in fp32.
+ * product (bf16, past one token: the activation is fp32 from approximate exponentials and reciprocals).
+ * rows < 2^31, C and hidden <= 2^20.  bf16 runs on the tensor cores (widths that are no multiple of 8
+ * through copies with padded rows in the workspace, the weights' too, made in every call), fp32 on CUDA
+ * cores in fp32.
  * The workspace holds a chunk of tokens' hidden values; the size dsa3d_gated_ffn_workspace_bytes
  * returns covers min(rows, 65536) tokens, and any workspace of at least the size for min(rows, 256)
  * works (tokens are then processed in more chunks).  The sizes never go down with rows (one workspace for
@@ -358,8 +360,10 @@ dsa3d_status_t dsa3d_gated_ffn(const void *x, const void *gate_weight, const voi
  * Backward of dsa3d_gated_ffn for the upstream gradient dy [rows][C], from x alone: the forward keeps
  * nothing of [rows][hidden] (two such tensors would be larger than the GPU's memory at long-video
  * sizes), so x Wg and x Wu are formed again.
- *   dx [rows][C], dgate_weight, dup_weight [C][hidden], ddown_weight [hidden][C], I/O type (written;
- *   sums over tokens are fp32, rounded once).  add's gradient is dy itself.
+ *   dx [rows][C], dgate_weight, dup_weight [C][hidden], ddown_weight [hidden][C], I/O type (written).
+ *   add's gradient is dy itself.  The hidden values h = act(x Wg) * (x Wu) and the gradients of x Wg and
+ *   x Wu are rounded to the I/O type as operands of the products that give these outputs; the outputs' own
+ *   sums are fp32, rounded once.
  * The workspace rule is the forward's, with dsa3d_gated_ffn_backward_workspace_bytes; the smallest
  * workspace is the size for min(rows, 256) plus 12 * C256 * hidden256 + 1024 bytes, the widths rounded up
  * to multiples of 256 (the weight gradients' sums over the chunks).  The weight gradients may
