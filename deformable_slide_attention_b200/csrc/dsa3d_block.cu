@@ -30,8 +30,10 @@ struct NormPlan {
   size_t smem;
 };
 // Two vectors per thread where a row has more than a warp's 32: fewer threads to sum over, and weights
-// that still fit in registers.  odd_per: the same for rows read element by element (30,000 x 1001 fp32:
-// forward 62 us at 8, 66 and more at 2; backward 103 at 4, 110 at 2).
+// that still fit in registers.  odd_per: the same for rows read element by element, one number for both
+// types.  30,000 x 1001: forward, 8 of them: fp32 62 us (66 and more at 2), bf16 with a sum 109 (111 at 4);
+// backward, 4 of them and four blocks per SM: fp32 103 (110 at 2; 91 at 8 with three blocks), bf16 109 (141 to
+// 150 at 8).
 NormPlan norm_plan(int C, dsa3d_dtype_t dtype, int odd_per) {
   NormPlan p{};
   const int vec = dtype == DSA3D_F32 ? 4 : 8;

@@ -187,9 +187,11 @@ struct Carver {
   }
 };
 
-// A forward of so few tokens that the weights' bytes bind, with rows of whole 16-byte vectors.  C 4096,
-// hidden 10,944: bf16, one token 57 us against 70 through the tensor-core tiles, two 99 against 70; fp32,
-// four tokens 137 us against 987 through the tiles of 64 rows.
+// A forward of so few tokens that the weights' bytes bind, with rows of whole 16-byte vectors.  bf16, us
+// through the vector products against the tensor-core tiles: one token 57 against 70 at C 4096, hidden 10,944,
+// 25 against 38 at 2048 x 5464, 20.7 against 22 at 512 x 2048; two tokens 81 against 70, 35 against 38, 20.5
+// against 22, so the tiles take two (1024 x 4096: 26 where the vector products need 21).  fp32 at 4096 x
+// 10,944: four tokens 136 us against 987 through the tiles of 64 rows.
 bool few_rows(const Ffn& f) {
   const int v = f.f32() ? 4 : 8;
   return f.rows <= (f.f32() ? kRowsMaxF32 : kRowsMaxBf16) && f.C % v == 0 && f.hidden % v == 0;

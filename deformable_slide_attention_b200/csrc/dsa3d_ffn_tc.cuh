@@ -28,7 +28,7 @@
 // The products are bound by the tensor cores (6 or 16 rows C hidden operations against a few bytes per
 // element).  Four 720p frames (14,400 x 2048), hidden 5464, TFLOP/s over a long run under the power cap:
 // hidden values 1300, y 1260, their backward 980, dx 1280, weight gradients 1290; a library product of
-// these sizes 1150 to 1200 and 1430 at 8192^3.  The tensor pipe is busy 80 to 88% of the cycles, 62% in
+// these sizes 1150 to 1200 and 1430 at 8192^3.  The tensor pipe is busy 80 to 88% of the cycles, 64% in
 // kTcHiddenBwd.  Waits are bounded (dsa3d_tc.cuh); no load is multicast.
 #pragma once
 

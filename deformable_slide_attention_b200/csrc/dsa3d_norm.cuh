@@ -254,8 +254,8 @@ __device__ __forceinline__ void ring_rows(Vec<T, V> (&v)[R][PER], const RowRing<
 // Block: TX * TY threads; group ty takes R consecutive rows per step.  nv = C / V vectors per row,
 // nv <= TX * PER.  The next step's rows are loaded into registers before this step's are reduced: the
 // two reductions and their barriers would otherwise leave HBM idle.  Bound by HBM where rows are wide:
-// 115,200 x 2048 bf16, residual sum included, 299 us (6.3 TB/s, 96% of a copy's rate; without the sum
-// 178 us, 81%: the element-wise work, halved by packed pairs, is then half the issue slots).
+// 115,200 x 2048 bf16, residual sum included, 299 to 312 us (6.0 to 6.3 TB/s, 92 to 96% of a copy's rate;
+// without the sum 178 to 182 us, 80%: the element-wise work, halved by packed pairs, is then half the issue slots).
 template <typename T, int V, int PER, int R, bool ADD>
 __global__ void __launch_bounds__(norm_max_threads(PER, R)) dsa3d_layer_norm_kernel(
     const T* x, const T* add_to, const float* __restrict__ weight, const float* __restrict__ bias,
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(norm_max_threads(PER, R)) dsa3d_layer_norm_ker
 // dx, and per block one row of partial sums [2][C] (dw, db) at partial + blockIdx.x * 2 * C when
 // weight is not null.  RING: rows come through a RowRing (the column sums leave no registers for rows in
 // flight); else plain loads, for odd widths and rows too wide for it.  115,200 x 2048 bf16 with the
-// residual gradient: 308 us (6.1 TB/s, 93% of a copy's rate); plain loads 332 us at best.
+// residual gradient: 308 to 318 us (5.9 to 6.1 TB/s, 90 to 93% of a copy's rate); plain loads 332 us at best.
 template <typename T, int V, int PER, int R, bool ADD, bool RING>
 __global__ void __launch_bounds__(norm_max_threads(PER, R)) dsa3d_layer_norm_bwd_kernel(
     const T* __restrict__ h, const float* __restrict__ weight, const float* __restrict__ stats,
